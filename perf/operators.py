@@ -247,7 +247,7 @@ def _plain_train(s):
     rho, iota, a, beta, h = _forward(s)
     x = s["x"].float()
     before = torch.cat([s["h0"].unsqueeze(1), h[:, :-1]], 1)
-    dh = s["dout"].float()
+    dh = s["dout"].to(torch.float32, copy=True)
     dh[:, -1] += s["dlast"]
     later = torch.cat([a[:, 1:], torch.zeros_like(a[:, :1])], 1)  # a of the step after
     g = _recur(later.flip(1), dh.flip(1)).flip(1)
