@@ -31,6 +31,10 @@
  *                          MambaMini" Steps 2-4): a sequence scanned in
  *                          independent pieces (with _aggregate_rec /
  *                          _from_rec, the pieces' inner carries kept).
+ *   gated_scan_fwd, gated_scan_bwd, gated_state_update; rms_norm_fwd,
+ *   rms_norm_fp8, rms_norm_bwd; fp8_quantize, fp8_quantize_weight, fp8_linear
+ *                          The operators of a residual layer around a
+ *                          recurrence (their own section below).
  *
  * Conventions shared by every entry point:
  *   - Tensor pointers are DEVICE pointers owned by the caller; the library
@@ -467,6 +471,178 @@ int selective_scan_bwd_ex(const void* u, const void* delta, const float* A,
 
 /* Bytes of the ckpt buffer for dims (a negative ssm_status if dims are invalid). */
 int64_t ssm_ckpt_bytes(const ssm_dims* dims);
+
+/* ---------------------------------------------------------------------------
+ * Operators of the residual layer around a recurrence: the gated linear
+ * recurrence (one state number per channel), the root-mean-square norm with
+ * the residual's addition and an 8-bit output, and the linear product of 8-bit
+ * operands with block scales.
+ *
+ * Conventions as above, with these differences:
+ *   - Scratch is the caller's: an entry point that needs it has a _bytes query
+ *     (0 where the sizes need none, a negative ssm_status where they are
+ *     invalid) and takes a `work` pointer to that many bytes, 16-byte aligned,
+ *     uninitialised, not shared with a call that may overlap.  These entry
+ *     points allocate nothing and can be captured into a graph.
+ *   - Activations need only their element's alignment unless said otherwise.
+ *   - Values that are not finite propagate; a reset drops them (below).
+ * ------------------------------------------------------------------------- */
+
+/* Sizes of a gated recurrence.  x, r and i are rows of dim channels (unit
+ * channel stride); consecutive rows, over the whole [batch][seqlen], are
+ * ld_x, ld_r and ld_i elements apart (>= dim), so the three may be column
+ * slices of one projection's output.  Every other array is contiguous. */
+typedef struct {
+  int64_t batch;
+  int64_t seqlen;
+  int64_t dim;
+  int64_t ld_x;
+  int64_t ld_r;
+  int64_t ld_i;
+  int32_t dtype;   /* ssm_dtype of x, r, i, out, dout, dx, dr, di */
+} gated_dims;
+
+/*
+ * Gated linear recurrence over a sequence, per channel:
+ *   rho_t = sigmoid(r_t), iota_t = sigmoid(i_t),
+ *   a_t = exp(log_decay * rho_t), beta_t = sqrt(1 - a_t^2),
+ *   h_t = a_t h_{t-1} + beta_t iota_t x_t,  out_t = h_t.
+ *   x, r, i   : [batch][seqlen][dim] of dtype, row strides above
+ *   log_decay : [dim] float32, <= 0 (beta is taken as 0 where 1 - a^2 < 0)
+ *   reset     : [batch][seqlen] bytes (nullable): where nonzero a document
+ *               starts, a_t = 0 and beta_t = 1, and h_{t-1} is dropped even if
+ *               it is not finite
+ *   h0        : [batch][dim] float32 (nullable = zeros)
+ *   out       : [batch][seqlen][dim] of dtype (nullable if ckpt is given)
+ *   last_state: [batch][dim] float32 (nullable), h after the last step
+ *   ckpt      : gated_ckpt_bytes(dims) bytes (nullable): the float32 states the
+ *               backward starts from
+ *   work      : gated_scan_work_bytes(dims) bytes
+ * The result does not depend on how many workgroups run at a time: the carries
+ * between pieces of a sequence are folded in one order.
+ */
+int64_t gated_scan_work_bytes(const gated_dims* dims);
+int64_t gated_ckpt_bytes(const gated_dims* dims);
+int gated_scan_fwd(const void* x, const void* r, const void* i,
+                   const float* log_decay, const uint8_t* reset,
+                   const float* h0, void* out, float* last_state, float* ckpt,
+                   void* work, const gated_dims* dims, void* stream);
+
+/*
+ * Backward of gated_scan_fwd: the gradients of sum dout*out + sum
+ * dlast*last_state.
+ *   dout         : [batch][seqlen][dim] of dtype
+ *   dlast        : [batch][dim] float32 (nullable = zeros)
+ *   ckpt         : what gated_scan_fwd left for the same inputs; NULL makes the
+ *                  call run that forward itself
+ *   dx, dr, di   : [batch][seqlen][dim] of dtype, contiguous
+ *   dlog_decay   : [dim] float32
+ *   dh0          : [batch][dim] float32 (nullable)
+ *   work         : gated_scan_bwd_work_bytes(dims, ckpt != NULL) bytes
+ * Where beta_t = 0 (r_t = -inf, or log_decay = 0) the derivative of beta_t,
+ * which has no finite value there, counts as 0.
+ */
+int64_t gated_scan_bwd_work_bytes(const gated_dims* dims, int has_ckpt);
+int gated_scan_bwd(const void* x, const void* r, const void* i,
+                   const float* log_decay, const uint8_t* reset,
+                   const float* h0, const void* dout, const float* dlast,
+                   const float* ckpt, void* dx, void* dr, void* di,
+                   float* dlog_decay, float* dh0, void* work,
+                   const gated_dims* dims, void* stream);
+
+/*
+ * One step of the same recurrence on a stored state [batch][dim] (float32,
+ * updated in place): x, r, i and out are [batch][dim] (row strides of x, r, i
+ * as given); dims->seqlen must be 1.
+ */
+int gated_state_update(float* state, const void* x, const void* r,
+                       const void* i, const float* log_decay, void* out,
+                       const gated_dims* dims, void* stream);
+
+/* Sizes of a norm: rows of dim values.  dim at most 16384. */
+typedef struct {
+  int64_t rows;
+  int64_t dim;
+  int32_t dtype;           /* ssm_dtype of x, y, dy */
+  int32_t residual_dtype;  /* ssm_dtype of residual, residual_out, s, dres, ds */
+} norm_dims;
+
+/*
+ * Root-mean-square norm of a row, with the residual's addition in front:
+ *   s = x + residual,  y = s / sqrt(mean(s^2) + eps) * weight.
+ *   x            : [rows][dim] of dtype
+ *   residual     : [rows][dim] of residual_dtype (nullable: s = x)
+ *   weight       : [dim] float32
+ *   eps          : > 0
+ *   residual_out : [rows][dim] of residual_dtype, s as the next layer's
+ *                  residual; may be residual itself.  Given exactly when
+ *                  residual is.  y is computed from s before that rounding.
+ * rms_norm_fwd writes y in dtype.  rms_norm_fp8 writes it in 8 bits
+ * (OCP e4m3) with a float32 scale for every 128 values of a row:
+ *   m = max(max |y| in the group, 2^-100),  q = e4m3(448 y / m),
+ *   scale = m / 448,  y ~ q * scale
+ *   q            : [rows][dim] bytes
+ *   scale        : [ceil(dim / 128)][rows] float32
+ * and needs dim a multiple of 16 and x, residual, weight, residual_out and q
+ * 16-byte aligned.  fp8_quantize writes x itself in that form.
+ */
+int rms_norm_fwd(const void* x, const void* residual, const float* weight,
+                 float eps, void* y, void* residual_out, const norm_dims* dims,
+                 void* stream);
+int rms_norm_fp8(const void* x, const void* residual, const float* weight,
+                 float eps, void* q, float* scale, void* residual_out,
+                 const norm_dims* dims, void* stream);
+int fp8_quantize(const void* x, void* q, float* scale, const norm_dims* dims,
+                 void* stream);
+
+/*
+ * Backward of rms_norm_fwd with respect to s (the gradient of both x and
+ * residual) and weight:
+ *   s       : [rows][dim] of residual_dtype, the normalised sum (residual_out,
+ *             or x with residual_dtype = dtype)
+ *   dres    : [rows][dim] of residual_dtype (nullable), the gradient that
+ *             reaches s on the residual's own way, added to ds
+ *   ds      : [rows][dim] of residual_dtype
+ *   dweight : [dim] float32
+ *   work    : rms_norm_bwd_work_bytes(dims) bytes
+ */
+int64_t rms_norm_bwd_work_bytes(const norm_dims* dims);
+int rms_norm_bwd(const void* dy, const void* s, const float* weight, float eps,
+                 const void* dres, void* ds, float* dweight, void* work,
+                 const norm_dims* dims, void* stream);
+
+/*
+ * Weight [n][k] (a linear layer's layout, dtype) in 8 bits with a float32 scale
+ * for every tile of 128 x 128 (the last ones smaller), by the rule of
+ * rms_norm_fp8 over the tile: q [n][k], scale [ceil(n / 128)][ceil(k / 128)].
+ */
+int fp8_quantize_weight(const void* w, int dtype, int64_t n, int64_t k,
+                        void* q, float* scale, void* stream);
+
+/* Sizes of a linear product. */
+typedef struct {
+  int64_t rows;    /* M, tokens */
+  int64_t n;       /* outputs */
+  int64_t k;       /* inputs, a multiple of 16 */
+  int32_t dtype;   /* ssm_dtype of out */
+} linear_dims;
+
+/*
+ * Linear layer on 8-bit operands, summed in float32 (with SSM_BF16 outputs, 128
+ * inputs at a time by the 8-bit matrix instruction, which keeps about 13 bits
+ * below their largest product; with SSM_F32 outputs, to float32's precision):
+ *   out[m][n] = sum_k xq[m][k] x_scale[k/128][m] wq[n][k] w_scale[n/128][k/128]
+ *               + bias[n]
+ *   xq [rows][k], x_scale [ceil(k/128)][rows]           (rms_norm_fp8, fp8_quantize)
+ *   wq [n][k], w_scale [ceil(n/128)][ceil(k/128)]       (fp8_quantize_weight)
+ *   bias : [n] float32 (nullable);  out : [rows][n] of dtype
+ *   work : fp8_linear_work_bytes(dims) bytes
+ * xq and wq must be 16-byte aligned.
+ */
+int64_t fp8_linear_work_bytes(const linear_dims* dims);
+int fp8_linear(const void* xq, const float* x_scale, const void* wq,
+               const float* w_scale, const float* bias, void* out, void* work,
+               const linear_dims* dims, void* stream);
 
 /* Static, human-readable name of a status code (never NULL). */
 const char* ssm_status_string(int status);

@@ -15,3 +15,15 @@ from .api import (  # noqa: F401
     check_device_errors,
     fwd_plan,
 )
+from .layer import (  # noqa: F401
+    gated_scan_fwd,
+    gated_scan_bwd,
+    gated_ckpt_buffer,
+    gated_state_update,
+    rms_norm_fwd,
+    rms_norm_fp8,
+    rms_norm_bwd,
+    fp8_quantize,
+    fp8_quantize_weight,
+    fp8_linear,
+)

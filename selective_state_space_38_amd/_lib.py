@@ -43,6 +43,20 @@ EXPORTED = (
     "causal_conv1d_fwd",
     "causal_conv1d_update",
     "mamba_block_fwd",
+    "gated_scan_work_bytes",
+    "gated_ckpt_bytes",
+    "gated_scan_fwd",
+    "gated_scan_bwd_work_bytes",
+    "gated_scan_bwd",
+    "gated_state_update",
+    "rms_norm_fwd",
+    "rms_norm_fp8",
+    "fp8_quantize",
+    "rms_norm_bwd_work_bytes",
+    "rms_norm_bwd",
+    "fp8_quantize_weight",
+    "fp8_linear_work_bytes",
+    "fp8_linear",
     "ssm_status_string",
     "ssm_check_device_errors",
     "ssm_fwd_plan_for",
@@ -89,6 +103,29 @@ class MambaBlockDims(ctypes.Structure):
         ("d_state", ctypes.c_int64),
         ("dt_rank", ctypes.c_int64),
         ("conv_width", ctypes.c_int32),
+        ("dtype", ctypes.c_int32),
+    ]
+
+
+class GatedDims(ctypes.Structure):
+    _fields_ = [(name, ctypes.c_int64) for name in
+                ("batch", "seqlen", "dim", "ld_x", "ld_r", "ld_i")] + [("dtype", ctypes.c_int32)]
+
+
+class NormDims(ctypes.Structure):
+    _fields_ = [
+        ("rows", ctypes.c_int64),
+        ("dim", ctypes.c_int64),
+        ("dtype", ctypes.c_int32),
+        ("residual_dtype", ctypes.c_int32),
+    ]
+
+
+class LinearDims(ctypes.Structure):
+    _fields_ = [
+        ("rows", ctypes.c_int64),
+        ("n", ctypes.c_int64),
+        ("k", ctypes.c_int64),
         ("dtype", ctypes.c_int32),
     ]
 
@@ -190,6 +227,29 @@ def load():
     lib.mamba_block_fwd.argtypes = [vp, ctypes.POINTER(MambaBlockWeights), vp,
                                     ctypes.POINTER(MambaBlockDims), vp]
     lib.mamba_block_fwd.restype = ctypes.c_int
+    i64 = ctypes.c_int64
+    gated_p, norm_p = ctypes.POINTER(GatedDims), ctypes.POINTER(NormDims)
+    linear_p = ctypes.POINTER(LinearDims)
+    for name, args in (
+            ("gated_scan_work_bytes", [gated_p]),
+            ("gated_ckpt_bytes", [gated_p]),
+            ("gated_scan_bwd_work_bytes", [gated_p, ctypes.c_int]),
+            ("rms_norm_bwd_work_bytes", [norm_p]),
+            ("fp8_linear_work_bytes", [linear_p])):
+        getattr(lib, name).argtypes = args
+        getattr(lib, name).restype = i64
+    for name, args in (
+            ("gated_scan_fwd", [vp] * 10 + [gated_p, vp]),
+            ("gated_scan_bwd", [vp] * 15 + [gated_p, vp]),
+            ("gated_state_update", [vp] * 6 + [gated_p, vp]),
+            ("rms_norm_fwd", [vp] * 3 + [ctypes.c_float] + [vp] * 2 + [norm_p, vp]),
+            ("rms_norm_fp8", [vp] * 3 + [ctypes.c_float] + [vp] * 3 + [norm_p, vp]),
+            ("fp8_quantize", [vp] * 3 + [norm_p, vp]),
+            ("rms_norm_bwd", [vp] * 3 + [ctypes.c_float] + [vp] * 4 + [norm_p, vp]),
+            ("fp8_quantize_weight", [vp, ctypes.c_int, i64, i64, vp, vp, vp]),
+            ("fp8_linear", [vp] * 7 + [linear_p, vp])):
+        getattr(lib, name).argtypes = args
+        getattr(lib, name).restype = ctypes.c_int
     lib.ssm_status_string.argtypes = [ctypes.c_int]
     lib.ssm_status_string.restype = ctypes.c_char_p
     lib.ssm_check_device_errors.argtypes = [vp]

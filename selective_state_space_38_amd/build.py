@@ -25,6 +25,10 @@ SOURCES = [
     ("carry.hip", "carry", []),
     ("conv1d.hip", "conv1d", []),
     ("gemm.hip", "gemm", []),
+    ("layer_api.hip", "layer_api", []),
+    ("gated_scan.hip", "gated_scan", []),
+    ("rms_norm.hip", "rms_norm", []),
+    ("fp8_linear.hip", "fp8_linear", []),
 ]
 
 HIPCC_FLAGS = [
