@@ -33,91 +33,586 @@ __device__ __forceinline__ void gate(float r, float lam2, float& rho, float& a, 
   beta = __builtin_amdgcn_sqrtf(fmaxf(m * (2.0f - m), 0.0f));
 }
 
-template <typename T>
-__global__ __launch_bounds__(64) void gated_fwd_kernel(GatedArgs p) {
-  const int64_t g = static_cast<int64_t>(blockIdx.x) * 64 + threadIdx.x;
-  const int64_t D = p.dim, L = p.seqlen;
-  if (g >= p.batch * D) return;
-  const int64_t b = g / D, c = g - b * D;
-  const T* x = static_cast<const T*>(p.x) + b * L * p.ld_x + c;
-  const T* r = static_cast<const T*>(p.r) + b * L * p.ld_r + c;
-  const T* in = static_cast<const T*>(p.i) + b * L * p.ld_i + c;
-  T* out = p.out ? static_cast<T*>(p.out) + b * L * D + c : nullptr;
-  const float lam2 = p.log_decay[c] * kLog2e;
-  float h = p.h0 ? p.h0[g] : 0.0f;
-  for (int64_t t = 0; t < L; ++t) {
-    if (p.ckpt && t % kGatedRun == 0)
-      p.ckpt[(b * div_up64(L, kGatedRun) + t / kGatedRun) * D + c] = h;
-    float rho, a, beta;
-    gate(to_f32(r[t * p.ld_r]), lam2, rho, a, beta);
-    const float ix = sigmoid_f32(to_f32(in[t * p.ld_i])) * to_f32(x[t * p.ld_x]);
-    h = (p.reset && p.reset[b * L + t]) ? ix : fmaf(a, h, beta * ix);
-    if (out) store_act(out, t * D, h);
-  }
-  if (p.last_state) p.last_state[g] = h;
+// A wave owns V channels per lane (one dword of a row: 64 float32 or 128
+// bfloat16 channels, 256 bytes) and a run of kGatedRun steps; a workgroup is
+// up to kWaves consecutive runs of the same channels, a chunk of the sequence.
+// One pass over the run's gates and inputs leaves two numbers per step in
+// registers, the product A_j of a since the run's start and the state H_j from
+// zero; the runs' last ones meet in LDS, and once the state h before the run is
+// known the outputs are A_j h + H_j.  Every input is read once and every output
+// written once.
+//
+// Chunks of one channel block exchange carries through 8-byte records, one per
+// channel, holding both numbers of an aggregate or the state itself, so a
+// relaxed 8-byte load sees a whole record and nothing else is ordered.  A
+// workgroup publishes its aggregate, walks back to the nearest state and folds
+// the aggregates since then forward, h = A h + H, in sequence order.  Since a
+// chunk's state is that same fold, where the walk stops does not change a bit
+// of the result.  Work is taken in ticket order, chunk by chunk, so a wait is
+// always for a workgroup that already runs.
+constexpr int kWaves = 8;
+constexpr int kChunk = kWaves * kGatedRun;
+
+// Record: state (code 1.0, sign clear) or aggregate (code -A, sign set); 0 is
+// empty.
+constexpr uint32_t kStateCode = 0x3f800000u;
+
+__device__ __forceinline__ void put_record(uint64_t* p, uint32_t code, float h) {
+  __hip_atomic_store(p, (static_cast<uint64_t>(code) << 32) | __float_as_uint(h), __ATOMIC_RELAXED,
+                     __HIP_MEMORY_SCOPE_AGENT);
 }
 
-// part: [batch][dim] dlog_decay of each batch row
-template <typename T>
-__global__ __launch_bounds__(64) void gated_bwd_kernel(GatedArgs p, float* part) {
-  const int64_t g = static_cast<int64_t>(blockIdx.x) * 64 + threadIdx.x;
-  const int64_t D = p.dim, L = p.seqlen;
-  if (g >= p.batch * D) return;
-  const int64_t b = g / D, c = g - b * D;
-  const T* x = static_cast<const T*>(p.x) + b * L * p.ld_x + c;
-  const T* r = static_cast<const T*>(p.r) + b * L * p.ld_r + c;
-  const T* in = static_cast<const T*>(p.i) + b * L * p.ld_i + c;
-  const T* dout = static_cast<const T*>(p.dout) + b * L * D + c;
-  T* dx = static_cast<T*>(p.dx) + b * L * D + c;
-  T* dr = static_cast<T*>(p.dr) + b * L * D + c;
-  T* di = static_cast<T*>(p.di) + b * L * D + c;
-  const float lam = p.log_decay[c], lam2 = lam * kLog2e;
-  float carry = p.dlast ? p.dlast[g] : 0.0f;
-  float dlam = 0.0f;
-  const int64_t runs = div_up64(L, kGatedRun);
-  for (int64_t q = runs - 1; q >= 0; --q) {
-    const int64_t t0 = q * kGatedRun;
-    const int n = static_cast<int>(L - t0 < kGatedRun ? L - t0 : kGatedRun);
-    float h = p.ckpt[(b * runs + q) * D + c];
-    float before[kGatedRun];
-    for (int j = 0; j < n; ++j) {
-      const int64_t t = t0 + j;
-      float rho, a, beta;
-      gate(to_f32(r[t * p.ld_r]), lam2, rho, a, beta);
-      const float ix = sigmoid_f32(to_f32(in[t * p.ld_i])) * to_f32(x[t * p.ld_x]);
-      before[j] = h;
-      h = (p.reset && p.reset[b * L + t]) ? ix : fmaf(a, h, beta * ix);
-    }
-    for (int j = n - 1; j >= 0; --j) {
-      const int64_t t = t0 + j;
-      float rho, a, beta;
-      gate(to_f32(r[t * p.ld_r]), lam2, rho, a, beta);
-      const float iota = sigmoid_f32(to_f32(in[t * p.ld_i])), xt = to_f32(x[t * p.ld_x]);
-      const bool cut = p.reset && p.reset[b * L + t];
-      const float gt = to_f32(dout[t * D]) + carry;
-      carry = cut ? 0.0f : a * gt;
-      const float bt = cut ? 1.0f : beta;
-      const float dxt = gt * bt * iota;
-      const float inv = beta > 0.0f ? rcp_hw(beta) : 0.0f;
-      const float da = cut ? 0.0f : carry * before[j] - (a * a * inv) * (gt * iota * xt);
-      const float dlr = da * rho;
-      store_act(dx, t * D, dxt);
-      store_act(di, t * D, dxt * xt * (1.0f - iota));
-      store_act(dr, t * D, dlr * lam * (1.0f - rho));
-      dlam += dlr;
-    }
-  }
-  if (p.dh0) p.dh0[g] = carry;
-  part[g] = dlam;
+template <int V>
+__device__ __forceinline__ void put_records(uint64_t* p, bool state, const float (&A)[V],
+                                            const float (&H)[V]) {
+#pragma unroll
+  for (int v = 0; v < V; ++v)
+    put_record(p + v, state ? kStateCode : (__float_as_uint(A[v]) | 0x80000000u), H[v]);
 }
 
-__global__ __launch_bounds__(64) void gated_sum_kernel(const float* part, int64_t rows, int64_t dim,
-                                                       float* out) {
-  const int64_t c = static_cast<int64_t>(blockIdx.x) * 64 + threadIdx.x;
-  if (c >= dim) return;
+// The state after chunk `newest` of a channel block, from its records (rec:
+// this lane's record of chunk 0; consecutive chunks are 64 V apart).  Chunk 0
+// always publishes its state, so the walk ends there at the latest.
+template <int V>
+__device__ __forceinline__ void look_back(const uint64_t* rec, int newest, int spin_limit,
+                                          float (&h)[V]) {
+  constexpr int K = 8 / V;  // records in flight per channel
+  uint64_t win[K][V];
+  auto load = [&](int base) {
+#pragma unroll
+    for (int k = 0; k < K; ++k)
+#pragma unroll
+      for (int v = 0; v < V; ++v)
+        win[k][v] = __hip_atomic_load(
+            rec + static_cast<int64_t>(base - k > 0 ? base - k : 0) * (64 * V) + v,
+            __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  };
+  int base = newest;
+  for (bool late = false;;) {
+    bool found;
+    for (int spins = 0;;) {
+      load(base);
+      bool ready = true;
+      found = true;
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        bool f = false;
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+          ready = ready && (f || win[k][v] != 0);
+          f = f || (win[k][v] != 0 && (win[k][v] >> 63) == 0);
+        }
+        found = found && f;
+      }
+      if (__all(ready)) break;
+      if (spins++ >= spin_limit) {
+        late = true;
+        if ((threadIdx.x & 63) == 0) atomicAdd(&g_gated_timeouts, 1u);
+        break;
+      }
+      __builtin_amdgcn_s_sleep(1);
+    }
+    if (late || __all(found) || base < K) break;
+    base -= K;
+  }
+#pragma unroll
+  for (int v = 0; v < V; ++v) h[v] = 0.0f;
+  for (;;) {
+#pragma unroll
+    for (int k = K - 1; k >= 0; --k) {
+      if (base - k < 0) continue;
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        const uint32_t code = static_cast<uint32_t>(win[k][v] >> 32);
+        const float H = __uint_as_float(static_cast<uint32_t>(win[k][v]));
+        h[v] = (code >> 31) ? fmaf(__uint_as_float(code & 0x7fffffffu), h[v], H) : H;
+      }
+    }
+    if (base == newest) return;
+    base += K;
+    load(base);
+  }
+}
+
+// R rows of V channels per lane as loaded; rows past the last (n of them)
+// repeat it.  base and ld are the wave's, off is the lane's byte offset.
+template <typename T, int V, int R>
+struct Rows {
+  uint32_t w[R];
+  __device__ __forceinline__ void load(const void* base, int64_t elem0, int64_t ld, uint32_t off,
+                                       int n) {
+    const T* row = static_cast<const T*>(base) + elem0;
+#pragma unroll
+    for (int j = 0; j < R; ++j) {
+      const T* p = add_bytes(row, off);
+      row += j + 1 < n ? ld : 0;
+      if constexpr (sizeof(T) * V == 4)
+        w[j] = *reinterpret_cast<const uint32_t*>(p);
+      else
+        w[j] = *p;
+    }
+  }
+  __device__ __forceinline__ float get(int j, int v) const {
+    if constexpr (sizeof(T) == 4) return __uint_as_float(w[j]);
+    return __uint_as_float(V == 2 && v == 1 ? (w[j] & 0xffff0000u) : (w[j] << 16));
+  }
+};
+
+template <typename T, int V>
+__device__ __forceinline__ void store_row(void* base, int64_t elem, uint32_t off,
+                                          const float (&v)[V]) {
+  T* p = add_bytes(static_cast<T*>(base) + elem, off);
+  if constexpr (V == 2)
+    *reinterpret_cast<uint32_t*>(p) = pack_bf16x2(v[0], v[1]);
+  else
+    store_act(p, 0, v[0]);
+}
+
+// Where a wave works: one run of one channel block.
+struct Place {
+  int64_t b, t0;     // batch row, first step
+  int64_t c0;        // first channel of the block
+  int n;             // steps (<= 0: none)
+  int chain, chunk;  // channel block over all batch rows; chunk in order of work
+};
+
+struct GatedGrid {
+  int n_cblk, chains, chunks, waves;
+  int* ticket;
+  uint64_t* rec;
+  float* part;       // backward: dlog_decay of every (batch row, chunk), [..][dim]
+};
+
+template <int R, bool MULTI, bool REVERSE>
+__device__ __forceinline__ Place find_place(const GatedArgs& p, const GatedGrid& g, int w,
+                                            int* lds_ticket) {
+  int task = blockIdx.x;
+  if (MULTI) {
+    if (threadIdx.x == 0) *lds_ticket = atomicAdd(g.ticket, 1);
+    __syncthreads();
+    task = __builtin_amdgcn_readfirstlane(*lds_ticket);
+  }
+  Place q;
+  q.chunk = task / g.chains;
+  q.chain = task - q.chunk * g.chains;
+  q.b = q.chain / g.n_cblk;
+  q.c0 = static_cast<int64_t>(q.chain - static_cast<int>(q.b) * g.n_cblk);
+  const int64_t run = static_cast<int64_t>(REVERSE ? g.chunks - 1 - q.chunk : q.chunk) * g.waves + w;
+  q.t0 = run * R;
+  const int64_t left = p.seqlen - q.t0;
+  q.n = left < R ? static_cast<int>(left) : R;
+  return q;
+}
+
+// Bit j: step j of the run starts a document.
+__device__ __forceinline__ uint32_t reset_bits(const GatedArgs& p, const Place& q, int lane) {
+  const bool on = lane < q.n && p.reset[q.b * p.seqlen + q.t0 + (lane < q.n ? lane : 0)] != 0;
+  return static_cast<uint32_t>(__ballot(on));
+}
+
+template <typename T, int V, bool RESET, bool MULTI>
+__global__ __launch_bounds__(64 * kWaves) void gated_fwd_kernel(GatedArgs p, GatedGrid g) {
+  constexpr int R = kGatedRun;
+  __shared__ float2 s_agg[kWaves][64 * V];  // product of a, state from zero
+  __shared__ float s_carry[64 * V];
+  __shared__ uint32_t s_cut[kWaves];        // the run holds a reset
+  __shared__ int s_ticket;
+  const int lane = threadIdx.x & 63;
+  const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int64_t D = p.dim, L = p.seqlen;
+  Place q = find_place<R, MULTI, false>(p, g, w, &s_ticket);
+  q.c0 *= 64 * V;
+  const bool live = q.c0 + lane * V < D;
+  const int64_t c = live ? q.c0 + lane * V : D - V;  // a dead lane repeats the last channels
+  const uint32_t off = static_cast<uint32_t>((c - q.c0) * static_cast<int64_t>(sizeof(T)));
+  const int n = q.n;
+
+  float lam2[V];
+#pragma unroll
+  for (int v = 0; v < V; ++v) lam2[v] = p.log_decay[c + v] * kLog2e;
+  float first[V];  // the state before the sequence
+#pragma unroll
+  for (int v = 0; v < V; ++v) first[v] = p.h0 ? p.h0[q.b * D + c + v] : 0.0f;
+
+  float A[R][V], H[R][V];
+  uint32_t cut = 0;
+  if (n > 0) {
+    const int64_t row = q.b * L + q.t0;
+    Rows<T, V, R> x, r, in;
+    r.load(p.r, row * p.ld_r + q.c0, p.ld_r, off, n);
+    in.load(p.i, row * p.ld_i + q.c0, p.ld_i, off, n);
+    x.load(p.x, row * p.ld_x + q.c0, p.ld_x, off, n);
+    if (RESET) cut = reset_bits(p, q, lane);
+#pragma unroll
+    for (int j = 0; j < R; ++j) {
+      const bool at_reset = RESET && (cut >> j & 1);
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        float rho, a, beta;
+        gate(r.get(j, v), lam2[v], rho, a, beta);
+        const float ix = sigmoid_f32(in.get(j, v)) * x.get(j, v);
+        if (at_reset) {
+          A[j][v] = 0.0f;
+          H[j][v] = ix;
+        } else if (j == 0) {
+          A[j][v] = a;
+          H[j][v] = beta * ix;
+        } else {
+          A[j][v] = A[j - 1][v] * a;
+          H[j][v] = fmaf(a, H[j - 1][v], beta * ix);
+        }
+      }
+    }
+    if (n < R) {  // steps past the end leave the state alone
+#pragma unroll
+      for (int j = 1; j < R; ++j)
+        if (j >= n) {
+#pragma unroll
+          for (int v = 0; v < V; ++v) {
+            A[j][v] = A[j - 1][v];
+            H[j][v] = H[j - 1][v];
+          }
+        }
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < R; ++j)
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        A[j][v] = 1.0f;
+        H[j][v] = 0.0f;
+      }
+  }
+  const int W = g.waves;
+  if (MULTI || W > 1) {
+#pragma unroll
+    for (int v = 0; v < V; ++v) s_agg[w][lane * V + v] = make_float2(A[R - 1][v], H[R - 1][v]);
+    if (RESET && lane == 0) s_cut[w] = cut;
+    lds_barrier();
+  }
+  // state after the runs before run `upto`, from state h before the chunk
+  auto fold = [&](int upto, float (&h)[V]) {
+    for (int k = 0; k < upto; ++k) {
+      const bool drop = RESET && s_cut[k];
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        const float2 ag = s_agg[k][lane * V + v];
+        h[v] = drop ? ag.y : fmaf(ag.x, h[v], ag.y);
+      }
+    }
+  };
+  float h[V];
+  if (MULTI) {
+    if (w == 0) {
+      uint64_t* rec = g.rec + (static_cast<int64_t>(q.chain) * g.chunks) * (64 * V) + lane * V;
+      uint64_t* own = rec + static_cast<int64_t>(q.chunk) * (64 * V);
+      float cA[V], cH[V];
+      bool drop_any = false;
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        cA[v] = 1.0f;
+        cH[v] = 0.0f;
+      }
+      for (int k = 0; k < W; ++k) {
+        const bool drop = RESET && s_cut[k];
+        drop_any = drop_any || drop;
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+          const float2 ag = s_agg[k][lane * V + v];
+          cH[v] = drop ? ag.y : fmaf(ag.x, cH[v], ag.y);
+          cA[v] *= ag.x;
+        }
+      }
+      const bool last = q.chunk == g.chunks - 1;
+      if (q.chunk == 0) {
+#pragma unroll
+        for (int v = 0; v < V; ++v) h[v] = first[v];
+      } else {
+        // after a reset the chunk's end does not depend on what came before
+        if (!last) put_records<V>(own, drop_any, cA, cH);
+        look_back<V>(rec, q.chunk - 1, p.spin_limit, h);
+      }
+      if (!last && !(drop_any && q.chunk)) {
+        float end[V];
+#pragma unroll
+        for (int v = 0; v < V; ++v) end[v] = drop_any ? cH[v] : fmaf(cA[v], h[v], cH[v]);
+        put_records<V>(own, true, cA, end);
+      }
+#pragma unroll
+      for (int v = 0; v < V; ++v) s_carry[lane * V + v] = h[v];
+    }
+    lds_barrier();
+#pragma unroll
+    for (int v = 0; v < V; ++v) h[v] = s_carry[lane * V + v];
+    fold(w, h);
+  } else {
+#pragma unroll
+    for (int v = 0; v < V; ++v) h[v] = first[v];
+    if (W > 1) fold(w, h);
+  }
+  if (n <= 0 || !live) return;
+  if (p.ckpt) {
+    float* ck = p.ckpt + (q.b * div_up64(L, R) + q.t0 / R) * D + c;
+#pragma unroll
+    for (int v = 0; v < V; ++v) ck[v] = h[v];
+  }
+  const int64_t row = q.b * L + q.t0;
+  float o[V];
+#pragma unroll
+  for (int j = 0; j < R; ++j) {
+    // after a reset the state before the run does not count, finite or not
+    const bool since = RESET && (cut & ((2u << j) - 1)) != 0;
+#pragma unroll
+    for (int v = 0; v < V; ++v) o[v] = since ? H[j][v] : fmaf(A[j][v], h[v], H[j][v]);
+    if (p.out && j < n) store_row<T, V>(p.out, (row + j) * D + q.c0, off, o);
+  }
+  if (p.last_state && q.t0 + n == L) {
+#pragma unroll
+    for (int v = 0; v < V; ++v) p.last_state[q.b * D + c + v] = o[v];
+  }
+}
+
+// Backward.  With g_t the gradient of h_t: g_t = dout_t + c_{t+1}, c_t = a_t
+// g_t, c_L = dlast: the same recurrence from the end, on c.  A wave's run is
+// half a checkpoint's (kBwdRun steps, so that what the second pass needs of each
+// step, seven numbers, leaves two workgroups' registers on a CU): it recomputes
+// the gates into registers and the states from the checkpoint, the odd waves
+// through their even neighbour's aggregate.  c runs through the chunk and over
+// the chunks as h does forward (chunks are taken from the sequence's end).
+constexpr int kBwdRun = kGatedRun / 2;
+constexpr int kBwdChunk = kWaves * kBwdRun;
+
+template <typename T, int V, bool RESET, bool MULTI>
+__global__ __launch_bounds__(64 * kWaves, 4) void gated_bwd_kernel(GatedArgs p, GatedGrid g) {
+  constexpr int R = kBwdRun;
+  __shared__ float2 s_agg[kWaves][64 * V];
+  __shared__ float s_carry[64 * V];
+  __shared__ float s_mid[kWaves / 2][64 * V];  // state after an even wave's run
+  __shared__ uint32_t s_cut[kWaves];
+  __shared__ int s_ticket;
+  const int lane = threadIdx.x & 63;
+  const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int64_t D = p.dim, L = p.seqlen;
+  Place q = find_place<R, MULTI, true>(p, g, w, &s_ticket);
+  q.c0 *= 64 * V;
+  const bool live = q.c0 + lane * V < D;
+  const int64_t c = live ? q.c0 + lane * V : D - V;
+  const uint32_t off = static_cast<uint32_t>((c - q.c0) * static_cast<int64_t>(sizeof(T)));
+  const int n = q.n;
+  const int64_t row = q.b * L + q.t0;
+
+  float lam[V], last[V];
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    lam[v] = p.log_decay[c + v];
+    last[v] = p.dlast ? p.dlast[q.b * D + c + v] : 0.0f;
+  }
+  Rows<T, V, R> x, r, in, dout;
+  float rho[R][V], iota[R][V], a[R][V], beta[R][V], before[R][V], start[V];
+  float A[V], H[V];
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    A[v] = 1.0f;
+    H[v] = 0.0f;
+  }
+  uint32_t cut = 0;
+  if (n > 0) {
+    r.load(p.r, row * p.ld_r + q.c0, p.ld_r, off, n);
+    in.load(p.i, row * p.ld_i + q.c0, p.ld_i, off, n);
+    x.load(p.x, row * p.ld_x + q.c0, p.ld_x, off, n);
+    dout.load(p.dout, row * D + q.c0, D, off, n);
+    if (RESET) cut = reset_bits(p, q, lane);
+#pragma unroll
+    for (int v = 0; v < V; ++v)
+      start[v] = p.ckpt[(q.b * div_up64(L, kGatedRun) + q.t0 / kGatedRun) * D + c + v];
+#pragma unroll
+    for (int j = 0; j < R; ++j)
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        gate(r.get(j, v), lam[v] * kLog2e, rho[j][v], a[j][v], beta[j][v]);
+        iota[j][v] = sigmoid_f32(in.get(j, v));
+      }
+  }
+  // the states before each step, from the run's first
+  auto states = [&](float (&h)[V]) {
+#pragma unroll
+    for (int j = 0; j < R; ++j) {
+      const bool at_reset = RESET && (cut >> j & 1);
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        before[j][v] = h[v];
+        const float ix = iota[j][v] * x.get(j, v);
+        h[v] = at_reset ? ix : fmaf(a[j][v], h[v], beta[j][v] * ix);
+      }
+    }
+  };
+  const int W = g.waves;
+  if ((w & 1) == 0 && n > 0) {
+    states(start);
+#pragma unroll
+    for (int v = 0; v < V; ++v) s_mid[w >> 1][lane * V + v] = start[v];
+  }
+  if (W > 1) lds_barrier();
+  if ((w & 1) == 1 && n > 0) {
+#pragma unroll
+    for (int v = 0; v < V; ++v) start[v] = s_mid[w >> 1][lane * V + v];
+    states(start);
+  }
+  if (n > 0) {
+#pragma unroll
+    for (int j = R - 1; j >= 0; --j) {
+      const bool at_reset = RESET && (cut >> j & 1);
+      if (j >= n) continue;
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        H[v] = at_reset ? 0.0f : a[j][v] * (dout.get(j, v) + H[v]);
+        A[v] = at_reset ? 0.0f : A[v] * a[j][v];
+      }
+    }
+  }
+  if (MULTI || W > 1) {
+#pragma unroll
+    for (int v = 0; v < V; ++v) s_agg[w][lane * V + v] = make_float2(A[v], H[v]);
+    if (RESET && lane == 0) s_cut[w] = cut;
+    lds_barrier();
+  }
+  // c before the runs after run `from`, from c after the chunk
+  auto fold = [&](int from, float (&h)[V]) {
+    for (int k = W - 1; k > from; --k) {
+      const bool drop = RESET && s_cut[k];
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        const float2 ag = s_agg[k][lane * V + v];
+        h[v] = drop ? ag.y : fmaf(ag.x, h[v], ag.y);
+      }
+    }
+  };
+  float h[V];
+  if (MULTI) {
+    if (w == 0) {
+      uint64_t* rec = g.rec + (static_cast<int64_t>(q.chain) * g.chunks) * (64 * V) + lane * V;
+      uint64_t* own = rec + static_cast<int64_t>(q.chunk) * (64 * V);
+      float cA[V], cH[V];
+      bool drop_any = false;
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        cA[v] = 1.0f;
+        cH[v] = 0.0f;
+      }
+      for (int k = W - 1; k >= 0; --k) {
+        const bool drop = RESET && s_cut[k];
+        drop_any = drop_any || drop;
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+          const float2 ag = s_agg[k][lane * V + v];
+          cH[v] = drop ? ag.y : fmaf(ag.x, cH[v], ag.y);
+          cA[v] *= ag.x;
+        }
+      }
+      const bool final_chunk = q.chunk == g.chunks - 1;  // the sequence's first
+      if (q.chunk == 0) {
+#pragma unroll
+        for (int v = 0; v < V; ++v) h[v] = last[v];
+      } else {
+        if (!final_chunk) put_records<V>(own, drop_any, cA, cH);
+        look_back<V>(rec, q.chunk - 1, p.spin_limit, h);
+      }
+      if (!final_chunk && !(drop_any && q.chunk)) {
+        float end[V];
+#pragma unroll
+        for (int v = 0; v < V; ++v) end[v] = drop_any ? cH[v] : fmaf(cA[v], h[v], cH[v]);
+        put_records<V>(own, true, cA, end);
+      }
+#pragma unroll
+      for (int v = 0; v < V; ++v) s_carry[lane * V + v] = h[v];
+    }
+    lds_barrier();
+#pragma unroll
+    for (int v = 0; v < V; ++v) h[v] = s_carry[lane * V + v];
+    fold(w, h);
+  } else {
+#pragma unroll
+    for (int v = 0; v < V; ++v) h[v] = last[v];
+    if (W > 1) fold(w, h);
+  }
+  float dlam[V];
+#pragma unroll
+  for (int v = 0; v < V; ++v) dlam[v] = 0.0f;
+  if (n > 0) {
+#pragma unroll
+    for (int j = R - 1; j >= 0; --j) {
+      if (j >= n) continue;
+      const bool at_reset = RESET && (cut >> j & 1);
+      float dx[V], dr[V], di[V];
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        const float xt = x.get(j, v), io = iota[j][v], be = beta[j][v], al = a[j][v];
+        const float gt = dout.get(j, v) + h[v];
+        const float gi = gt * io;
+        h[v] = at_reset ? 0.0f : al * gt;
+        dx[v] = at_reset ? gi : gi * be;
+        di[v] = dx[v] * xt * (1.0f - io);
+        const float inv = be > 0.0f ? rcp_hw(be) : 0.0f;
+        const float da = at_reset ? 0.0f : fmaf(h[v], before[j][v], -(al * al * inv) * (gi * xt));
+        const float dl = da * rho[j][v];
+        dr[v] = dl * lam[v] * (1.0f - rho[j][v]);
+        dlam[v] += dl;
+      }
+      if (live) {
+        store_row<T, V>(p.dx, (row + j) * D + q.c0, off, dx);
+        store_row<T, V>(p.dr, (row + j) * D + q.c0, off, dr);
+        store_row<T, V>(p.di, (row + j) * D + q.c0, off, di);
+      }
+    }
+    if (p.dh0 && q.t0 == 0 && live) {
+#pragma unroll
+      for (int v = 0; v < V; ++v) p.dh0[q.b * D + c + v] = h[v];
+    }
+  }
+  // the workgroup's dlog_decay, run by run
+  lds_barrier();  // s_agg was read by every wave's fold
+#pragma unroll
+  for (int v = 0; v < V; ++v) s_agg[w][lane * V + v].x = dlam[v];
+  lds_barrier();
+  if (w == 0 && live) {
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      float sum = 0.0f;
+      for (int k = 0; k < W; ++k) sum += s_agg[k][lane * V + v].x;
+      g.part[(q.b * g.chunks + q.chunk) * D + c + v] = sum;
+    }
+  }
+}
+
+// out[c] = sum over rows of part[row][c]: 16 waves take every 16th row each,
+// eight loads in flight, and their sums are added in order.
+__global__ __launch_bounds__(1024) void gated_sum_kernel(const float* part, int64_t rows,
+                                                         int64_t dim, float* out) {
+  __shared__ float lds[16][64];
+  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
+  const int64_t c = static_cast<int64_t>(blockIdx.x) * 64 + lane;
+  const int64_t cc = c < dim ? c : dim - 1;
   float s = 0.0f;
-  for (int64_t q = 0; q < rows; ++q) s += part[q * dim + c];
+  int64_t q = w;
+  for (; q + 7 * 16 < rows; q += 8 * 16) {
+    float t[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) t[k] = part[(q + k * 16) * dim + cc];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) s += t[k];
+  }
+  for (; q < rows; q += 16) s += part[q * dim + cc];
+  lds[w][lane] = s;
+  __syncthreads();
+  if (w || c >= dim) return;
+  s = 0.0f;
+  for (int k = 0; k < 16; ++k) s += lds[k][lane];
   out[c] = s;
+}
+
+__global__ __launch_bounds__(256) void gated_clear_kernel(uint4* p, int64_t n) {
+  const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+  if (i < n) p[i] = make_uint4(0, 0, 0, 0);
 }
 
 template <typename T>
@@ -134,30 +629,93 @@ __global__ __launch_bounds__(256) void gated_step_kernel(GatedArgs p) {
   store_act(static_cast<T*>(p.out), g, h);
 }
 
-int64_t gated_fwd_work(int, int64_t, int64_t, int64_t) { return 0; }
-int64_t gated_bwd_work(int, int64_t batch, int64_t, int64_t dim) { return batch * dim * 4; }
-
 static unsigned blocks_of(int64_t n, int64_t per) {
   return static_cast<unsigned>(div_up64(n, per));
 }
 
+// Channels per lane: two where rows can be moved in whole dwords of bfloat16
+// (an even dim and row strides, 4-byte aligned rows), else one.
+static int channels_per_lane(const GatedArgs& a) {
+  if (a.dtype == 0) return 1;
+  if ((a.dim | a.ld_x | a.ld_r | a.ld_i) & 1) return 1;
+  for (const void* q : {a.x, a.r, a.i, static_cast<const void*>(a.out), a.dout,
+                        static_cast<const void*>(a.dx), static_cast<const void*>(a.dr),
+                        static_cast<const void*>(a.di)})
+    if (reinterpret_cast<uintptr_t>(q) & 3) return 1;
+  return 2;
+}
+
+// Scratch of a pass over chunks: a ticket (16 bytes) and the records, for the
+// wider of the two channel layouts' padding.
+static int64_t record_bytes(int64_t batch, int64_t seqlen, int64_t dim, int chunk) {
+  const int64_t chunks = div_up64(seqlen, chunk);
+  return chunks <= 1 ? 0 : 16 + batch * chunks * div_up64(dim, 128) * 128 * 8;
+}
+
+int64_t gated_fwd_work(int, int64_t batch, int64_t seqlen, int64_t dim) {
+  return record_bytes(batch, seqlen, dim, kChunk);
+}
+int64_t gated_bwd_work(int, int64_t batch, int64_t seqlen, int64_t dim) {
+  return record_bytes(batch, seqlen, dim, kBwdChunk) +
+         batch * div_up64(seqlen, kBwdChunk) * dim * 4;
+}
+
+static GatedGrid grid_of(const GatedArgs& a, int v, int run, hipStream_t stream) {
+  const int chunk = kWaves * run;
+  GatedGrid g = {};
+  g.n_cblk = static_cast<int>(div_up64(a.dim, 64 * v));
+  g.chains = static_cast<int>(a.batch) * g.n_cblk;
+  g.chunks = static_cast<int>(div_up64(a.seqlen, chunk));
+  g.waves = g.chunks > 1 ? kWaves : static_cast<int>(div_up64(a.seqlen, run));
+  const int64_t bytes = record_bytes(a.batch, a.seqlen, a.dim, chunk);
+  if (bytes) {
+    g.ticket = static_cast<int*>(a.work);
+    g.rec = reinterpret_cast<uint64_t*>(static_cast<char*>(a.work) + 16);
+    gated_clear_kernel<<<blocks_of(bytes / 16, 256), 256, 0, stream>>>(
+        static_cast<uint4*>(a.work), bytes / 16);
+  }
+  g.part = reinterpret_cast<float*>(static_cast<char*>(a.work) + bytes);
+  return g;
+}
+
+#define SSM_LAUNCH_GATED(KERNEL)                                                            \
+  do {                                                                                      \
+    const dim3 grid(static_cast<unsigned>(g.chains) * static_cast<unsigned>(g.chunks));     \
+    const dim3 block(64 * g.waves);                                                         \
+    if (a.dtype == 0) {                                                                     \
+      SSM_LAUNCH_GATED_T(KERNEL, float, 1);                                                 \
+    } else if (v == 2) {                                                                    \
+      SSM_LAUNCH_GATED_T(KERNEL, bf16_t, 2);                                                \
+    } else {                                                                                \
+      SSM_LAUNCH_GATED_T(KERNEL, bf16_t, 1);                                                \
+    }                                                                                       \
+  } while (0)
+#define SSM_LAUNCH_GATED_T(KERNEL, T, V)                                                    \
+  if (g.chunks > 1) {                                                                       \
+    if (a.reset)                                                                            \
+      KERNEL<T, V, true, true><<<grid, block, 0, stream>>>(a, g);                           \
+    else                                                                                    \
+      KERNEL<T, V, false, true><<<grid, block, 0, stream>>>(a, g);                          \
+  } else {                                                                                  \
+    if (a.reset)                                                                            \
+      KERNEL<T, V, true, false><<<grid, block, 0, stream>>>(a, g);                          \
+    else                                                                                    \
+      KERNEL<T, V, false, false><<<grid, block, 0, stream>>>(a, g);                         \
+  }
+
 hipError_t launch_gated_fwd(const GatedArgs& a, hipStream_t stream) {
-  const unsigned grid = blocks_of(a.batch * a.dim, 64);
-  if (a.dtype == 0)
-    gated_fwd_kernel<float><<<grid, 64, 0, stream>>>(a);
-  else
-    gated_fwd_kernel<bf16_t><<<grid, 64, 0, stream>>>(a);
+  const int v = channels_per_lane(a);
+  const GatedGrid g = grid_of(a, v, kGatedRun, stream);
+  SSM_LAUNCH_GATED(gated_fwd_kernel);
   return hipGetLastError();
 }
 
 hipError_t launch_gated_bwd(const GatedArgs& a, hipStream_t stream) {
-  const unsigned grid = blocks_of(a.batch * a.dim, 64);
-  float* part = static_cast<float*>(a.work);
-  if (a.dtype == 0)
-    gated_bwd_kernel<float><<<grid, 64, 0, stream>>>(a, part);
-  else
-    gated_bwd_kernel<bf16_t><<<grid, 64, 0, stream>>>(a, part);
-  gated_sum_kernel<<<blocks_of(a.dim, 64), 64, 0, stream>>>(part, a.batch, a.dim, a.dlog_decay);
+  const int v = channels_per_lane(a);
+  const GatedGrid g = grid_of(a, v, kBwdRun, stream);
+  SSM_LAUNCH_GATED(gated_bwd_kernel);
+  gated_sum_kernel<<<blocks_of(a.dim, 64), 1024, 0, stream>>>(g.part, a.batch * g.chunks, a.dim,
+                                                              a.dlog_decay);
   return hipGetLastError();
 }
 
