@@ -3,8 +3,7 @@
 //   a = exp(log_decay rho), beta = sqrt(1 - a^2),
 //   h_t = a h_{t-1} + beta iota x_t.
 
-#include "layer_internal.h"
-#include "ssm_device.h"
+#include "layer_device.h"
 
 namespace ssm {
 
@@ -586,7 +585,7 @@ __global__ __launch_bounds__(64 * kWaves, 4) void gated_bwd_kernel(GatedArgs p, 
 
 // out[c] = sum over rows of part[row][c]: 16 waves take every 16th row each,
 // eight loads in flight, and their sums are added in order.
-__global__ __launch_bounds__(1024) void gated_sum_kernel(const float* part, int64_t rows,
+__global__ __launch_bounds__(1024) void column_sum_kernel(const float* part, int64_t rows,
                                                          int64_t dim, float* out) {
   __shared__ float lds[16][64];
   const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
@@ -631,6 +630,11 @@ __global__ __launch_bounds__(256) void gated_step_kernel(GatedArgs p) {
 
 static unsigned blocks_of(int64_t n, int64_t per) {
   return static_cast<unsigned>(div_up64(n, per));
+}
+
+void launch_column_sum(const float* part, int64_t rows, int64_t dim, float* out,
+                       hipStream_t stream) {
+  column_sum_kernel<<<blocks_of(dim, 64), 1024, 0, stream>>>(part, rows, dim, out);
 }
 
 // Channels per lane: two where rows can be moved in whole dwords of bfloat16
@@ -714,8 +718,7 @@ hipError_t launch_gated_bwd(const GatedArgs& a, hipStream_t stream) {
   const int v = channels_per_lane(a);
   const GatedGrid g = grid_of(a, v, kBwdRun, stream);
   SSM_LAUNCH_GATED(gated_bwd_kernel);
-  gated_sum_kernel<<<blocks_of(a.dim, 64), 1024, 0, stream>>>(g.part, a.batch * g.chunks, a.dim,
-                                                              a.dlog_decay);
+  launch_column_sum(g.part, a.batch * g.chunks, a.dim, a.dlog_decay, stream);
   return hipGetLastError();
 }
 

@@ -1,0 +1,69 @@
+// Device helpers shared by the residual layer's kernels.
+#pragma once
+
+#include "layer_internal.h"
+#include "ssm_device.h"
+
+namespace ssm {
+
+// v's exchange with the lane `ROR` places further in its row of 16.
+template <int ROR>
+__device__ __forceinline__ float row_ror(float v) {
+  return __builtin_bit_cast(
+      float, __builtin_amdgcn_mov_dpp(__builtin_bit_cast(int, v), 0x120 + ROR, 0xF, 0xF, true));
+}
+
+// Sum and maximum over a row of 16 lanes, in every lane.
+__device__ __forceinline__ float row16_sum(float v) {
+  v += row_ror<8>(v);
+  v += row_ror<4>(v);
+  v += row_ror<2>(v);
+  v += row_ror<1>(v);
+  return v;
+}
+__device__ __forceinline__ float row16_max(float v) {
+  v = fmaxf(v, row_ror<8>(v));
+  v = fmaxf(v, row_ror<4>(v));
+  v = fmaxf(v, row_ror<2>(v));
+  v = fmaxf(v, row_ror<1>(v));
+  return v;
+}
+
+__device__ __forceinline__ float read_lane(float v, int lane) {
+  return __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, v), lane));
+}
+
+// Sum over the wave, in every lane.
+__device__ __forceinline__ float wave_sum(float v) {
+  v = row16_sum(v);
+  return (read_lane(v, 0) + read_lane(v, 16)) + (read_lane(v, 32) + read_lane(v, 48));
+}
+
+// Values of a group on the 8-bit scale: 448 y / m by a reciprocal and one
+// correction.  m's mantissa and exponent are taken apart, so nothing
+// overflows and the reciprocal is of a number in [1/2, 1); 448 = 2^10 7/16 and
+// the product with 7/16 is exact for a bfloat16 y.  The correction leaves the
+// quotient within half a unit, so one on a tie between two 8-bit values stays
+// there.
+struct Fp8Scaler {
+  float mant, rcp;
+  int exp;
+  __device__ __forceinline__ explicit Fp8Scaler(float m)
+      : mant(__builtin_amdgcn_frexp_mantf(m)),
+        rcp(rcp_hw(mant)),
+        exp(10 - __builtin_amdgcn_frexp_expf(m)) {}
+  __device__ __forceinline__ float operator()(float y) const {
+    const float a = y * 0.4375f;
+    const float t = a * rcp;
+    return __builtin_amdgcn_ldexpf(fmaf(fmaf(-t, mant, a), rcp, t), exp);
+  }
+};
+
+// Four floats rounded to e4m3 (nearest even), in the order given.
+__device__ __forceinline__ uint32_t pack_fp8x4(float a, float b, float c, float d) {
+  int v = __builtin_amdgcn_cvt_pk_fp8_f32(a, b, 0, false);
+  v = __builtin_amdgcn_cvt_pk_fp8_f32(c, d, v, true);
+  return static_cast<uint32_t>(v);
+}
+
+}  // namespace ssm

@@ -52,6 +52,10 @@ hipError_t launch_gated_step(const GatedArgs& a, hipStream_t stream);
 // Reads and clears the count of carry waits that timed out (synchronises).
 hipError_t read_and_clear_gated_errors(hipStream_t stream, unsigned* count);
 
+// out[c] = sum over rows of part[row][c], in one fixed order.
+void launch_column_sum(const float* part, int64_t rows, int64_t dim, float* out,
+                       hipStream_t stream);
+
 struct NormArgs {
   int dtype, residual_dtype;
   int64_t rows, dim;
