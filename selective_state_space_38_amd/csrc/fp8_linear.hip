@@ -89,6 +89,249 @@ __global__ __launch_bounds__(64) void fp8_linear_kernel(LinearArgs p) {
   }
 }
 
+// ---- tiles: large M ----
+//
+// A workgroup computes BN outputs of BM tokens, a block of 128 inputs at a time.
+// Both operands' blocks go from global memory straight to LDS (16 bytes a lane),
+// two blocks' buffers in turn.  LDS rows are the 128 bytes of a row's block as 8
+// chunks of 16, chunk c at place c ^ key(row), so that the 8 lanes that read at a
+// time hit different banks.
+//
+// The weights are the matrix instruction's first operand, so a lane holds four
+// consecutive outputs of one token, and one multiplier (the token's scale times
+// the weight tile's) serves every result of a token column: four FMAs per matrix
+// instruction, issued one instruction later.  Weight row i of tile t is output
+// (t / 2) 32 + (i / 4) 8 + (t % 2) 4 + i % 4 of the wave's: two tiles give a lane
+// 8 consecutive outputs to store.
+//
+// The one barrier of a block stands before its last row of tiles, when every
+// operand of the block has been read from LDS: behind it the buffer takes the
+// block after next, and the next block's first operands are read while the last
+// row is multiplied.
+
+typedef const __attribute__((address_space(1))) void* global_ptr;
+typedef __attribute__((address_space(3))) void* lds_ptr;
+
+__device__ __forceinline__ int key_w(int row) { return (row & 3) | ((row >> 1) & 4); }
+__device__ __forceinline__ int key_x(int row) { return row & 7; }
+
+// What a lane loads for a place past a row's end.
+__device__ const uint4 g_zeros = {0, 0, 0, 0};
+
+// One operand's block of ROWS rows to LDS, 8 rows per wave at a time.
+template <int ROWS, int WAVES, bool WEIGHTS>
+struct Loader {
+  static constexpr int kRounds = ROWS / (8 * WAVES);
+  uint32_t off[kRounds];  // the lane's bytes, from the operand's rows and block
+  // place of the lane's chunk in a row's block, round j
+  __device__ __forceinline__ static int place(int j, int wave, int lane) {
+    const int r = (j * WAVES + wave) * 8 + (lane >> 3);
+    return ((lane & 7) ^ (WEIGHTS ? key_w(r) : key_x(r))) * 16;
+  }
+  __device__ __forceinline__ void init(int wave, int lane, int64_t row0, int64_t rows, int64_t k) {
+#pragma unroll
+    for (int j = 0; j < kRounds; ++j) {
+      const int r = (j * WAVES + wave) * 8 + (lane >> 3);
+      const int64_t row = row0 + r < rows ? r : rows - 1 - row0;  // past the end: the last row
+      off[j] = static_cast<uint32_t>(row * k + place(j, wave, lane));
+    }
+  }
+  // left: bytes of a row from the block's start; what lies past them is zero in LDS
+  __device__ __forceinline__ void load(const uint8_t* block, uint8_t* lds, int wave, int lane,
+                                       int left) const {
+    if (left >= kFp8Group) {
+#pragma unroll
+      for (int j = 0; j < kRounds; ++j)
+        __builtin_amdgcn_global_load_lds((global_ptr)(block + off[j]),
+                                         (lds_ptr)(lds + (j * WAVES + wave) * 1024), 16, 0, 0);
+    } else {
+#pragma unroll
+      for (int j = 0; j < kRounds; ++j) {
+        const uint8_t* from = block + off[j];
+        if (place(j, wave, lane) >= left) from = reinterpret_cast<const uint8_t*>(&g_zeros);
+        __builtin_amdgcn_global_load_lds((global_ptr)from,
+                                         (lds_ptr)(lds + (j * WAVES + wave) * 1024), 16, 0, 0);
+      }
+    }
+  }
+};
+
+// A lane's 32 bytes of a row's block, as two chunks.  One sum of integers per
+// access: the compiler then still sees which LDS object it is in.
+__device__ __forceinline__ i32x8 read_lds(const uint8_t* obj, uint32_t lo, uint32_t hi) {
+  const int4 u = *reinterpret_cast<const int4*>(obj + lo);
+  const int4 v = *reinterpret_cast<const int4*>(obj + hi);
+  return i32x8{u.x, u.y, u.z, u.w, v.x, v.y, v.z, v.w};
+}
+
+// Place of the workgroup's tile: consecutive workgroups go to the 8 XCDs in
+// turn, so each XCD gets a range of tiles of its own, walked in strips of four
+// token tiles by all output tiles, so that the tiles an XCD has in flight share
+// their rows in its L2.
+__device__ __forceinline__ void tile_of(int64_t tiles_m, int64_t tiles_n, int64_t* tm, int64_t* tn) {
+  const int64_t tiles = tiles_m * tiles_n, bid = blockIdx.x;
+  const int64_t xcd = bid % 8, each = tiles / 8, more = tiles % 8;
+  const int64_t t = xcd * each + (xcd < more ? xcd : more) + bid / 8;
+  const int64_t strip = t / (4 * tiles_n), m0 = strip * 4;
+  const int64_t high = tiles_m - m0 < 4 ? tiles_m - m0 : 4, in = t - strip * 4 * tiles_n;
+  *tm = m0 + in % high;
+  *tn = in / high;
+}
+
+template <typename T, int BN, int BM, int WN, int WM>
+__global__ __launch_bounds__(64 * WN * WM) void fp8_tile_kernel(LinearArgs p) {
+  constexpr int WAVES = WN * WM, NT = BN / WN / 16, MT = BM / WM / 16;
+  constexpr bool EXACT = sizeof(T) == 4;
+  // separate objects, so that reads of one are known not to wait for loads into another
+  __shared__ __align__(1024) uint8_t s_w0[BN * kFp8Group];
+  __shared__ __align__(1024) uint8_t s_w1[BN * kFp8Group];
+  __shared__ __align__(1024) uint8_t s_x0[BM * kFp8Group];
+  __shared__ __align__(1024) uint8_t s_x1[BM * kFp8Group];
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wn = wave % WN, wm = wave / WN;
+  int64_t tm, tn;
+  tile_of(div_up64(p.rows, BM), div_up64(p.n, BN), &tm, &tn);
+  const int64_t n0 = tn * BN, m0 = tm * BM;
+  const int k = static_cast<int>(p.k);
+  const int groups = (k + kFp8Group - 1) / kFp8Group;
+
+  Loader<BN, WAVES, true> lw;
+  Loader<BM, WAVES, false> lx;
+  lw.init(wave, lane, n0, p.n, p.k);
+  lx.init(wave, lane, m0, p.rows, p.k);
+  const uint8_t* gw = p.wq + n0 * p.k;
+  const uint8_t* gx = p.xq + m0 * p.k;
+  const int64_t nw = n0 + wn * (BN / WN);  // the wave's first output, in one tile of weights
+  const float* sw = p.w_scale + (nw < p.n ? nw / kFp8Group : 0) * groups;
+  uint32_t sx_off[MT];  // bytes of the lane's tokens' scales in a block's row of them
+#pragma unroll
+  for (int m = 0; m < MT; ++m) {
+    const int64_t tok = m0 + (wm * MT + m) * 16 + (lane & 15);
+    sx_off[m] = static_cast<uint32_t>((tok < p.rows ? tok : p.rows - 1) * 4);
+  }
+
+  f32x4 acc[NT][MT];
+#pragma unroll
+  for (int n = 0; n < NT; ++n)
+#pragma unroll
+    for (int m = 0; m < MT; ++m) acc[n][m] = f32x4{};
+
+  lw.load(gw, s_w0, wave, lane, k);
+  lx.load(gx, s_x0, wave, lane, k);
+  // the multipliers of block 0, and the scales of block 1
+  float mult[MT], raw[MT];
+  const int second = groups > 1 ? 1 : 0;
+  float wscale = sw[second];
+#pragma unroll
+  for (int m = 0; m < MT; ++m) {
+    mult[m] = *add_bytes(p.x_scale, sx_off[m]) * sw[0];
+    raw[m] = *add_bytes(p.x_scale + second * p.rows, sx_off[m]);
+  }
+  __syncthreads();
+  if (groups > 1) {
+    lw.load(gw + kFp8Group, s_w1, wave, lane, k - kFp8Group);
+    lx.load(gx + kFp8Group, s_x1, wave, lane, k - kFp8Group);
+  }
+
+  const int i = lane & 15, quad = lane >> 4;
+  const int w_row = wn * (BN / WN) + (i >> 2) * 8 + (i & 3), x_row = wm * (BM / WM) + i;
+  const uint32_t w_lo = w_row * kFp8Group + ((quad * 2) ^ key_w(w_row)) * 16;
+  const uint32_t w_hi = w_row * kFp8Group + ((quad * 2 + 1) ^ key_w(w_row)) * 16;
+  const uint32_t x_lo = x_row * kFp8Group + ((quad * 2) ^ key_x(x_row)) * 16;
+  const uint32_t x_hi = x_row * kFp8Group + ((quad * 2 + 1) ^ key_x(x_row)) * 16;
+  // row tile n of the wave's weights, token tile m of its activations
+  auto read_w = [&](const uint8_t* obj, int n) {
+    const uint32_t at = ((n >> 1) * 32 + (n & 1) * 4) * kFp8Group;
+    return read_lds(obj, w_lo + at, w_hi + at);
+  };
+  auto read_x = [&](const uint8_t* obj, int m) {
+    const uint32_t at = m * 16 * kFp8Group;
+    return read_lds(obj, x_lo + at, x_hi + at);
+  };
+  i32x8 a[2], b[MT];
+#pragma unroll
+  for (int m = 0; m < MT; ++m) b[m] = read_x(s_x0, m);
+  a[0] = read_w(s_w0, 0);
+
+  // Block g from (cw, cx), its first operands already read; the next is in (ow,
+  // ox).  Product t's sums follow product t + 2, when its result is there, and
+  // the order is fixed as written (left to itself the compiler reads a row's
+  // operands just before they are needed).
+  auto step = [&](int g, uint8_t* cw, uint8_t* cx, const uint8_t* ow, const uint8_t* ox) {
+    f32x4 d[3];
+    auto add = [&](int t) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        acc[t / MT][t % MT][j] = fmaf(d[t % 3][j], mult[t % MT], acc[t / MT][t % MT][j]);
+      // the sum is taken here: moved past later products, it would keep their
+      // results in registers of their own
+      asm volatile("" : "+v"(acc[t / MT][t % MT]));
+    };
+#pragma unroll
+    for (int t = 0; t < NT * MT; ++t) {
+      const int n = t / MT, m = t % MT;
+      if (m == 0) {
+        if (n + 1 < NT) {
+          a[(n + 1) & 1] = read_w(cw, n + 1);
+        } else {
+          __syncthreads();
+          a[NT & 1] = read_w(ow, 0);
+        }
+      }
+      d[t % 3] = mfma_fp8<EXACT>(a[n & 1], b[m]);
+      if (n + 1 == NT) b[m] = read_x(ox, m);
+      if (t >= 2) add(t - 2);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    add(NT * MT - 2);
+    add(NT * MT - 1);
+#pragma unroll
+    for (int m = 0; m < MT; ++m) mult[m] = raw[m] * wscale;
+    const int late = g + 2 < groups ? g + 2 : groups - 1;
+    wscale = sw[late];
+#pragma unroll
+    for (int m = 0; m < MT; ++m) {
+      asm volatile("" : "+v"(sx_off[m]));  // stays an offset: no 64-bit sum per token
+      raw[m] = *add_bytes(p.x_scale + static_cast<int64_t>(late) * p.rows, sx_off[m]);
+    }
+    if (g + 2 < groups) {
+      const int at = (g + 2) * kFp8Group;
+      lw.load(gw + at, cw, wave, lane, k - at);
+      lx.load(gx + at, cx, wave, lane, k - at);
+    }
+  };
+  int g = 0;
+  for (; g + 1 < groups; g += 2) {
+    step(g, s_w0, s_x0, s_w1, s_x1);
+    step(g + 1, s_w1, s_x1, s_w0, s_x0);
+  }
+  if (g < groups) step(g, s_w0, s_x0, s_w1, s_x1);
+
+  // 8 consecutive outputs of a token at a time
+  const bool whole = p.n % 8 == 0 && reinterpret_cast<uintptr_t>(p.out) % 16 == 0;
+#pragma unroll
+  for (int t = 0; t < NT / 2; ++t) {
+    const int64_t n = nw + t * 32 + (lane >> 4) * 8;
+    if (n >= p.n) continue;
+    const int last = static_cast<int>(p.n - n < 8 ? p.n - n - 1 : 7);
+    float bias[8] = {};
+    if (p.bias) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) bias[e] = p.bias[n + (e < last ? e : last)];
+    }
+#pragma unroll
+    for (int m = 0; m < MT; ++m) {
+      const int64_t tok = m0 + (wm * MT + m) * 16 + (lane & 15);
+      if (tok >= p.rows) continue;
+      float v[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] = acc[t * 2 + e / 4][m][e % 4] + bias[e];
+      store_run<T, 8>(static_cast<T*>(p.out) + tok * p.n + n, v, whole, last);
+    }
+  }
+}
+
 // One workgroup per tile of 128 x 128 weights.
 template <typename T>
 __global__ __launch_bounds__(256) void quantize_weight_kernel(const T* w, int64_t n, int64_t k,
@@ -115,12 +358,22 @@ __global__ __launch_bounds__(256) void quantize_weight_kernel(const T* w, int64_
 
 int64_t fp8_linear_work(int64_t, int64_t, int64_t) { return 0; }
 
-hipError_t launch_fp8_linear(const LinearArgs& a, hipStream_t stream) {
-  const unsigned grid = static_cast<unsigned>(div_up64(a.n, 16) * div_up64(a.rows, 16));
-  if (a.dtype == 0)
-    fp8_linear_kernel<float><<<grid, 64, 0, stream>>>(a);
+template <typename T>
+static void launch_linear_typed(const LinearArgs& a, hipStream_t stream) {
+  constexpr int BM = sizeof(T) == 4 ? 128 : 256;
+  if (a.rows > 64)
+    fp8_tile_kernel<T, 256, BM, 2, 4>
+        <<<static_cast<unsigned>(div_up64(a.n, 256) * div_up64(a.rows, BM)), 512, 0, stream>>>(a);
   else
-    fp8_linear_kernel<bf16_t><<<grid, 64, 0, stream>>>(a);
+    fp8_linear_kernel<T>
+        <<<static_cast<unsigned>(div_up64(a.n, 16) * div_up64(a.rows, 16)), 64, 0, stream>>>(a);
+}
+
+hipError_t launch_fp8_linear(const LinearArgs& a, hipStream_t stream) {
+  if (a.dtype == 0)
+    launch_linear_typed<float>(a, stream);
+  else
+    launch_linear_typed<bf16_t>(a, stream);
   return hipGetLastError();
 }
 
