@@ -3,8 +3,9 @@
 //               xs[kb][m] ws[n/128][kb] sum_{k in kb} xq[m][k] wq[n][k]  (+ bias[n]),
 // and the weights' conversion to that form.
 
-#include "layer_internal.h"
-#include "ssm_device.h"
+#include <stdlib.h>
+
+#include "layer_device.h"
 
 namespace ssm {
 
@@ -46,46 +47,83 @@ __device__ __forceinline__ f32x4 mfma_fp8(i32x8 a, i32x8 b) {
   }
 }
 
-// The 32 bytes of a row that a lane holds, zero past the row's end and for
-// rows past the operand's.
-__device__ __forceinline__ i32x8 load_row(const uint8_t* base, int64_t row, int64_t rows, int64_t k,
-                                          int64_t at) {
+// ---- few tokens: the weights' stream ----
+//
+// With at most 32 tokens the weights' bytes bound the product, so each is read
+// once, straight into the matrix instruction's registers: a workgroup takes 16
+// rows of weights, its waves the blocks of 128 inputs in turn (a wave's lanes
+// read 4 x 32 bytes of each row's block, whole cache lines); the activations come
+// from the L2.  The waves' sums meet in LDS and are added in wave order.  8
+// tokens, 5120 x 2560 weights: 6.9 us, launch included, 3 us of it a call of any
+// size; 32 rows a workgroup measured 6.0 there, but 9.0 against 6.7 at 2560 x 5120,
+// where they leave most CUs idle, and more blocks in flight a wave nothing.
+
+__device__ __forceinline__ i32x8 load_row(const uint8_t* row, int at, int k) {
   i32x8 v = {};
-  if (row < rows) {
-    const uint8_t* p = base + row * k + at;
-    if (at < k) {
-      const int4 t = *reinterpret_cast<const int4*>(p);
-      v[0] = t.x; v[1] = t.y; v[2] = t.z; v[3] = t.w;
-    }
-    if (at + 16 < k) {
-      const int4 t = *reinterpret_cast<const int4*>(p + 16);
-      v[4] = t.x; v[5] = t.y; v[6] = t.z; v[7] = t.w;
-    }
+  if (at < k) {
+    const int4 t = *reinterpret_cast<const int4*>(row + at);
+    v[0] = t.x; v[1] = t.y; v[2] = t.z; v[3] = t.w;
+  }
+  if (at + 16 < k) {
+    const int4 t = *reinterpret_cast<const int4*>(row + at + 16);
+    v[4] = t.x; v[5] = t.y; v[6] = t.z; v[7] = t.w;
   }
   return v;
 }
 
-// One wave per 16 x 16 outputs; the weights are the first operand, so a lane
-// holds four consecutive outputs of one token.
-template <typename T>
-__global__ __launch_bounds__(64) void fp8_linear_kernel(LinearArgs p) {
-  const int lane = threadIdx.x, col = lane & 15, quad = lane >> 4;
-  const int64_t tiles_n = div_up64(p.n, 16);
-  const int64_t n0 = (blockIdx.x % tiles_n) * 16, m = (blockIdx.x / tiles_n) * 16 + col;
-  const int64_t groups = div_up64(p.k, kFp8Group);
-  f32x4 acc = {};
-  for (int64_t g = 0; g < groups; ++g) {
-    const int64_t at = g * kFp8Group + quad * 32;
-    const f32x4 d = mfma_fp8<sizeof(T) == 4>(load_row(p.wq, n0 + col, p.n, p.k, at),
-                                             load_row(p.xq, m, p.rows, p.k, at));
-    const float scale = m < p.rows ? p.x_scale[g * p.rows + m] * p.w_scale[n0 / kFp8Group * groups + g]
-                                   : 0.0f;
-    for (int j = 0; j < 4; ++j) acc[j] = fmaf(d[j], scale, acc[j]);
+template <typename T, int MT>
+__global__ __launch_bounds__(1024) void fp8_stream_kernel(LinearArgs p) {
+  constexpr bool EXACT = sizeof(T) == 4;
+  __shared__ f32x4 s_sum[16][MT][64];
+  const int lane = threadIdx.x & 63, i = lane & 15, quad = lane >> 4;
+  const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int W = blockDim.x >> 6;
+  const int k = static_cast<int>(p.k), groups = (k + kFp8Group - 1) / kFp8Group;
+  const int rows = static_cast<int>(p.rows);
+  const int64_t n0 = static_cast<int64_t>(blockIdx.x) * 16;
+  const uint8_t* wrow = p.wq + (n0 + i < p.n ? n0 + i : p.n - 1) * p.k;
+  const uint8_t* xrow[MT];
+  int tok[MT];
+#pragma unroll
+  for (int m = 0; m < MT; ++m) {
+    tok[m] = m * 16 + i < rows ? m * 16 + i : rows - 1;
+    xrow[m] = p.xq + tok[m] * p.k;
   }
-  if (m >= p.rows) return;
-  for (int j = 0; j < 4; ++j) {
-    const int64_t n = n0 + quad * 4 + j;
-    if (n < p.n) store_act(static_cast<T*>(p.out), m * p.n + n, acc[j] + (p.bias ? p.bias[n] : 0.0f));
+  const float* sw = p.w_scale + (n0 / kFp8Group) * groups;  // 16 rows lie in one tile
+  f32x4 acc[MT] = {};
+  for (int g = w; g < groups; g += W) {
+    const int at = g * kFp8Group + quad * 32;
+    const i32x8 a = load_row(wrow, at, k);
+    i32x8 b[MT];
+    float mult[MT];
+#pragma unroll
+    for (int m = 0; m < MT; ++m) {
+      b[m] = load_row(xrow[m], at, k);
+      mult[m] = p.x_scale[static_cast<int64_t>(g) * rows + tok[m]] * sw[g];
+    }
+#pragma unroll
+    for (int m = 0; m < MT; ++m) {
+      const f32x4 d = mfma_fp8<EXACT>(a, b[m]);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) acc[m][j] = fmaf(d[j], mult[m], acc[m][j]);
+    }
+  }
+#pragma unroll
+  for (int m = 0; m < MT; ++m) s_sum[w][m][lane] = acc[m];
+  __syncthreads();
+  const bool whole = p.n % 4 == 0 && reinterpret_cast<uintptr_t>(p.out) % (4 * sizeof(T)) == 0;
+  for (int t = w; t < MT; t += W) {
+    f32x4 v = s_sum[0][t][lane];
+    for (int q = 1; q < W; ++q) v += s_sum[q][t][lane];
+    const int m = t * 16 + i;
+    const int64_t n = n0 + quad * 4;
+    if (m >= rows || n >= p.n) continue;
+    const int last = static_cast<int>(p.n - n < 4 ? p.n - n - 1 : 3);
+    float o[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      o[j] = v[j] + (p.bias ? p.bias[n + (j < last ? j : last)] : 0.0f);
+    store_run<T, 4>(static_cast<T*>(p.out) + m * p.n + n, o, whole, last);
   }
 }
 
@@ -193,17 +231,21 @@ __global__ __launch_bounds__(64 * WN * WM) void fp8_tile_kernel(LinearArgs p) {
   int64_t tm, tn;
   tile_of(div_up64(p.rows, BM), div_up64(p.n, BN), &tm, &tn);
   const int64_t n0 = tn * BN, m0 = tm * BM;
-  const int k = static_cast<int>(p.k);
-  const int groups = (k + kFp8Group - 1) / kFp8Group;
+  // with the inputs split over gridDim.y workgroups: blocks first .. first + groups - 1
+  const int all = static_cast<int>(div_up64(p.k, kFp8Group)), part = blockIdx.y;
+  const int each = (all + gridDim.y - 1) / gridDim.y, first = part * each;
+  const int groups = all - first < each ? all - first : each;
+  const int k = static_cast<int>(p.k) - first * kFp8Group;  // inputs from the first block on
 
   Loader<BN, WAVES, true> lw;
   Loader<BM, WAVES, false> lx;
   lw.init(wave, lane, n0, p.n, p.k);
   lx.init(wave, lane, m0, p.rows, p.k);
-  const uint8_t* gw = p.wq + n0 * p.k;
-  const uint8_t* gx = p.xq + m0 * p.k;
+  const uint8_t* gw = p.wq + n0 * p.k + first * kFp8Group;
+  const uint8_t* gx = p.xq + m0 * p.k + first * kFp8Group;
+  const float* x_scale = p.x_scale + first * p.rows;
   const int64_t nw = n0 + wn * (BN / WN);  // the wave's first output, in one tile of weights
-  const float* sw = p.w_scale + (nw < p.n ? nw / kFp8Group : 0) * groups;
+  const float* sw = p.w_scale + (nw < p.n ? nw / kFp8Group : 0) * all + first;
   uint32_t sx_off[MT];  // bytes of the lane's tokens' scales in a block's row of them
 #pragma unroll
   for (int m = 0; m < MT; ++m) {
@@ -225,8 +267,8 @@ __global__ __launch_bounds__(64 * WN * WM) void fp8_tile_kernel(LinearArgs p) {
   float wscale = sw[second];
 #pragma unroll
   for (int m = 0; m < MT; ++m) {
-    mult[m] = *add_bytes(p.x_scale, sx_off[m]) * sw[0];
-    raw[m] = *add_bytes(p.x_scale + second * p.rows, sx_off[m]);
+    mult[m] = *add_bytes(x_scale, sx_off[m]) * sw[0];
+    raw[m] = *add_bytes(x_scale + second * p.rows, sx_off[m]);
   }
   __syncthreads();
   if (groups > 1) {
@@ -293,7 +335,7 @@ __global__ __launch_bounds__(64 * WN * WM) void fp8_tile_kernel(LinearArgs p) {
 #pragma unroll
     for (int m = 0; m < MT; ++m) {
       asm volatile("" : "+v"(sx_off[m]));  // stays an offset: no 64-bit sum per token
-      raw[m] = *add_bytes(p.x_scale + static_cast<int64_t>(late) * p.rows, sx_off[m]);
+      raw[m] = *add_bytes(x_scale + static_cast<int64_t>(late) * p.rows, sx_off[m]);
     }
     if (g + 2 < groups) {
       const int at = (g + 2) * kFp8Group;
@@ -309,27 +351,60 @@ __global__ __launch_bounds__(64 * WN * WM) void fp8_tile_kernel(LinearArgs p) {
   if (g < groups) step(g, s_w0, s_x0, s_w1, s_x1);
 
   // 8 consecutive outputs of a token at a time
-  const bool whole = p.n % 8 == 0 && reinterpret_cast<uintptr_t>(p.out) % 16 == 0;
+  auto store = [&](auto* out, const float* bias_of) {
+    using O = typename std::remove_reference<decltype(*out)>::type;
+    const bool whole = p.n % 8 == 0 && reinterpret_cast<uintptr_t>(out) % 16 == 0;
 #pragma unroll
-  for (int t = 0; t < NT / 2; ++t) {
-    const int64_t n = nw + t * 32 + (lane >> 4) * 8;
-    if (n >= p.n) continue;
-    const int last = static_cast<int>(p.n - n < 8 ? p.n - n - 1 : 7);
-    float bias[8] = {};
-    if (p.bias) {
+    for (int t = 0; t < NT / 2; ++t) {
+      const int64_t n = nw + t * 32 + quad * 8;
+      if (n >= p.n) continue;
+      const int last = static_cast<int>(p.n - n < 8 ? p.n - n - 1 : 7);
+      float bias[8] = {};
+      if (bias_of) {
 #pragma unroll
-      for (int e = 0; e < 8; ++e) bias[e] = p.bias[n + (e < last ? e : last)];
+        for (int e = 0; e < 8; ++e) bias[e] = bias_of[n + (e < last ? e : last)];
+      }
+#pragma unroll
+      for (int m = 0; m < MT; ++m) {
+        const int64_t tok = m0 + (wm * MT + m) * 16 + i;
+        if (tok >= p.rows) continue;
+        float v[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] = acc[t * 2 + e / 4][m][e % 4] + bias[e];
+        store_run<O, 8>(out + tok * p.n + n, v, whole, last);
+      }
     }
-#pragma unroll
-    for (int m = 0; m < MT; ++m) {
-      const int64_t tok = m0 + (wm * MT + m) * 16 + (lane & 15);
-      if (tok >= p.rows) continue;
-      float v[8];
-#pragma unroll
-      for (int e = 0; e < 8; ++e) v[e] = acc[t * 2 + e / 4][m][e % 4] + bias[e];
-      store_run<T, 8>(static_cast<T*>(p.out) + tok * p.n + n, v, whole, last);
+  };
+  if (gridDim.y == 1)
+    store(static_cast<T*>(p.out), p.bias);
+  else
+    store(static_cast<float*>(p.work) + part * p.rows * p.n, static_cast<const float*>(nullptr));
+}
+
+// Joins the parts of a product whose inputs were split, in order.
+template <typename T>
+__global__ __launch_bounds__(256) void fp8_join_kernel(LinearArgs p, int parts) {
+  const int64_t at = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) * 4, all = p.rows * p.n;
+  if (at >= all) return;
+  const float* part = static_cast<const float*>(p.work);
+  const int last = static_cast<int>(all - at < 4 ? all - at - 1 : 3);
+  float v[4] = {};
+  if (all % 4 == 0) {
+    for (int q = 0; q < parts; ++q) {
+      const float4 t = *reinterpret_cast<const float4*>(part + q * all + at);
+      v[0] += t.x; v[1] += t.y; v[2] += t.z; v[3] += t.w;
     }
+  } else {
+    for (int q = 0; q < parts; ++q)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) v[e] += part[q * all + at + (e < last ? e : last)];
   }
+  if (p.bias) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) v[e] += p.bias[(at + (e < last ? e : last)) % p.n];
+  }
+  const bool whole = all % 4 == 0 && reinterpret_cast<uintptr_t>(p.out) % (4 * sizeof(T)) == 0;
+  store_run<T, 4>(static_cast<T*>(p.out) + at, v, whole, last);
 }
 
 // One workgroup per tile of 128 x 128 weights.
@@ -356,17 +431,102 @@ __global__ __launch_bounds__(256) void quantize_weight_kernel(const T* w, int64_
   if (threadIdx.x == 0) scale[blockIdx.x] = m / kFp8Max;
 }
 
-int64_t fp8_linear_work(int64_t, int64_t, int64_t) { return 0; }
+enum Shape : int { kStream = 0, kTile64 = 1, kTile128 = 2, kTile256 = 3 };
+constexpr int64_t kStreamRows = 32;  // most tokens of the streaming kernel
+
+struct Plan {
+  int shape, parts;
+};
+
+static int forced(const char* name) {
+  const char* v = getenv(name);
+  return v && *v ? atoi(v) : -1;
+}
+
+// Few tokens stream the weights.  More take the largest tile of which there are
+// enough: with fewer tiles than CUs, the smaller tile's larger share of loads
+// costs less than the idle CUs (measured over 320 to 5120 outputs and 768 to
+// 5120 inputs: 160 tiles of 256 x 256 38 us where 640 of 128 x 128 take 46, but
+// 80 take 62 against 47; 320 of 128 x 128 27 us against 33 for 64 x 64, 160 37
+// against 33; float32 outputs, two workgroups of 128 x 128 on a CU matching 256 x
+// 256, 640 65 against 79, 320 77 against 74).
+//
+// 64 x 64 tiles may split the inputs into parts.  Measured: about 0.42 us a
+// block, and 2 us for the join plus its traffic, written and read at 2.5 TB/s;
+// the least sum of the two is taken.  SSM_FORCE_LINEAR_SHAPE and _PARTS override
+// (tests, tuning).
+static Plan plan_of(int dtype, int64_t rows, int64_t n, int64_t k) {
+  Plan q = {kStream, 1};
+  const int shape = forced("SSM_FORCE_LINEAR_SHAPE"), parts = forced("SSM_FORCE_LINEAR_PARTS");
+  const int64_t groups = div_up64(k, kFp8Group);
+  auto tiles = [&](int64_t side) { return div_up64(n, side) * div_up64(rows, side); };
+  if (rows > kStreamRows) {
+    if (dtype != 0 && tiles(256) >= 150) {
+      q.shape = kTile256;
+    } else if (tiles(128) >= (dtype == 0 ? 384 : 256)) {
+      q.shape = kTile128;
+    } else {
+      q.shape = kTile64;
+      double best = 0.0;
+      for (int t = 1; t <= 8 && t <= groups; ++t) {
+        const double blocks = static_cast<double>(div_up64(groups, t)) * div_up64(tiles(64) * t, 512);
+        const double us = 0.42 * blocks + (t > 1 ? 2.0 + 8e-6 / 2.5 * rows * n * t : 0.0);
+        if (t == 1 || us < best) {
+          best = us;
+          q.parts = t;
+        }
+      }
+    }
+  }
+  if (shape >= 0 && shape <= kTile256 && (shape != kStream || rows <= kStreamRows) &&
+      (shape != kTile256 || dtype != 0)) {
+    q.shape = shape;
+    q.parts = 1;
+  }
+  if (q.shape != kStream && parts > 0) q.parts = parts;
+  if (q.parts > groups) q.parts = static_cast<int>(groups);
+  // every part has a block: with each = ceil(groups / parts), drop the empty ones
+  q.parts = static_cast<int>(div_up64(groups, div_up64(groups, q.parts)));
+  return q;
+}
+
+int64_t fp8_linear_work(int dtype, int64_t rows, int64_t n, int64_t k) {
+  const Plan q = plan_of(dtype, rows, n, k);
+  return q.parts > 1 ? q.parts * rows * n * 4 : 0;
+}
+
+template <typename T, int MT>
+static void launch_stream(const LinearArgs& a, hipStream_t stream) {
+  const int64_t groups = div_up64(a.k, kFp8Group);
+  // up to 16 waves, as many as give each the same number of blocks
+  const int waves = static_cast<int>(div_up64(groups, div_up64(groups, 16)));
+  fp8_stream_kernel<T, MT>
+      <<<static_cast<unsigned>(div_up64(a.n, 16)), 64 * waves, 0, stream>>>(a);
+}
+
+template <typename T, int BN, int BM, int WN, int WM>
+static void launch_tiles(const LinearArgs& a, int parts, hipStream_t stream) {
+  const dim3 grid(static_cast<unsigned>(div_up64(a.n, BN) * div_up64(a.rows, BM)), parts);
+  fp8_tile_kernel<T, BN, BM, WN, WM><<<grid, 64 * WN * WM, 0, stream>>>(a);
+  if (parts > 1)
+    fp8_join_kernel<T>
+        <<<static_cast<unsigned>(div_up64(a.rows * a.n, 1024)), 256, 0, stream>>>(a, parts);
+}
 
 template <typename T>
 static void launch_linear_typed(const LinearArgs& a, hipStream_t stream) {
-  constexpr int BM = sizeof(T) == 4 ? 128 : 256;
-  if (a.rows > 64)
-    fp8_tile_kernel<T, 256, BM, 2, 4>
-        <<<static_cast<unsigned>(div_up64(a.n, 256) * div_up64(a.rows, BM)), 512, 0, stream>>>(a);
-  else
-    fp8_linear_kernel<T>
-        <<<static_cast<unsigned>(div_up64(a.n, 16) * div_up64(a.rows, 16)), 64, 0, stream>>>(a);
+  const Plan q = plan_of(a.dtype, a.rows, a.n, a.k);
+  switch (q.shape) {
+    case kStream:
+      if (a.rows <= 16) launch_stream<T, 1>(a, stream);
+      else launch_stream<T, 2>(a, stream);
+      break;
+    case kTile64: launch_tiles<T, 64, 64, 2, 2>(a, q.parts, stream); break;
+    case kTile128: launch_tiles<T, 128, 128, 2, 2>(a, q.parts, stream); break;
+    default:
+      // bfloat16 outputs only (float32 ones' widened operands do not fit the registers)
+      if constexpr (sizeof(T) == 2) launch_tiles<T, 256, 256, 2, 4>(a, q.parts, stream);
+  }
 }
 
 hipError_t launch_fp8_linear(const LinearArgs& a, hipStream_t stream) {

@@ -339,7 +339,7 @@ int fp8_quantize_weight(const void* w, int dtype, int64_t n, int64_t k, void* q,
 
 int64_t fp8_linear_work_bytes(const linear_dims* dims) {
   const int rc = check_linear(dims);
-  return rc != SSM_OK ? rc : up16(ssm::fp8_linear_work(dims->rows, dims->n, dims->k));
+  return rc != SSM_OK ? rc : up16(ssm::fp8_linear_work(dims->dtype, dims->rows, dims->n, dims->k));
 }
 
 int fp8_linear(const void* xq, const float* x_scale, const void* wq, const float* w_scale,

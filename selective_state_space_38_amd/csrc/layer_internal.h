@@ -93,7 +93,7 @@ struct LinearArgs {
   void* work;
 };
 
-int64_t fp8_linear_work(int64_t rows, int64_t n, int64_t k);
+int64_t fp8_linear_work(int dtype, int64_t rows, int64_t n, int64_t k);
 hipError_t launch_fp8_linear(const LinearArgs& a, hipStream_t stream);
 hipError_t launch_quantize_weight(const void* w, int dtype, int64_t n, int64_t k, uint8_t* q,
                                   float* scale, hipStream_t stream);

@@ -341,3 +341,31 @@ def test_refusals():
         fp8_linear(*linear_inputs(4, 16, 24))
     with pytest.raises(RuntimeError):
         fp8_linear(args[0][:0], args[1][:, :0].contiguous(), *args[2:])
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("shape", [1, 2, 3])
+@pytest.mark.parametrize("m,n,k", [(1, 1, 16), (5, 130, 144), (65, 264, 400), (130, 72, 128),
+                                   (257, 300, 1296), (300, 520, 272), (513, 257, 2064)])
+def test_linear_tiles(m, n, k, shape, dtype, monkeypatch):
+    """Every tile shape, whole and with the inputs split into parts."""
+    from selective_state_space_38_amd import fp8_linear
+    args, bias = linear_inputs(m, n, k, seed=m), rand(n, seed=5)
+    monkeypatch.setenv("SSM_FORCE_LINEAR_SHAPE", str(shape))
+    for parts in (1, 2, 3, 7):
+        monkeypatch.setenv("SSM_FORCE_LINEAR_PARTS", str(parts))
+        for b in (None, bias):
+            check_linear(args, b, dtype, fp8_linear(*args, bias=b, out_dtype=dtype))
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_linear_output_alignment(dtype):
+    # an output that starts one element into its buffer, for every path
+    from selective_state_space_38_amd import fp8_linear
+    for m, n, k in ((3, 64, 256), (70, 128, 256), (1100, 1536, 128), (300, 64, 2048)):
+        args = linear_inputs(m, n, k)
+        buf = torch.full((m * n + 2,), 7.0, dtype=dtype, device="cuda")
+        out = buf[1:-1].view(m, n)
+        fp8_linear(*args, out_dtype=dtype, out=out)
+        assert torch.equal(out, fp8_linear(*args, out_dtype=dtype))
+        assert float(buf[0]) == float(buf[-1]) == 7.0
