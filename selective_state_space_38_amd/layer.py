@@ -6,15 +6,47 @@ As in ``api``: argument marshalling only.  Scratch comes from torch's caching
 allocator on the current stream, so the calls can be captured into a graph.
 """
 
-import ctypes
+import contextlib
+from ctypes import byref
 
 import torch
 
 from . import _lib
-from .api import _DTYPES, _check, _ptr, _raise, _stream
+from . import api
+from .api import _DTYPES, _raise
 
 FP8 = torch.float8_e4m3fn
 FP8_GROUP = 128
+
+# The calls for a few tokens last some microseconds, most of them here: the
+# checks below take the common case in one condition, and the device is entered
+# only where it is not the current one (entering it and torch's stream object
+# cost 1.3 and 1.9 us, these two 0.4 together).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_NO_CONTEXT = contextlib.nullcontext()
+
+
+def _on(device):
+    if device.index == torch.cuda.current_device():
+        return _NO_CONTEXT
+    return torch.cuda.device(device)
+
+
+def _stream(device):
+    if _raw_stream is not None:
+        return _raw_stream(device.index)
+    return torch.cuda.current_stream(device).cuda_stream
+
+
+def _ptr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _check(t, name, dtype, shape, device):
+    if t is None or (type(t) is torch.Tensor and t.dtype is dtype and t.shape == shape
+                     and t.device == device and t.is_contiguous()):
+        return
+    api._check(t, name, dtype, shape, device)
 
 
 def _act(t, name):
@@ -32,15 +64,18 @@ def _row_stride(t, name, dtype, shape, device):
     """Elements between consecutive rows of t, whose last dimension is
     contiguous and whose other dimensions step evenly (a contiguous tensor, or
     column slices of one)."""
+    dim = shape[-1]
+    if type(t) is torch.Tensor and t.dtype is dtype and t.shape == shape \
+            and t.device == device and t.is_contiguous():
+        return dim
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.device != device:
         raise ValueError(f"{name} is on {t.device}, expected {device}")
     if t.dtype != dtype:
         raise ValueError(f"{name} has dtype {t.dtype}, expected {dtype}")
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
-    dim = shape[-1]
     if t.is_contiguous():
         return dim
     strides = t.stride()
@@ -61,6 +96,11 @@ def _row_stride(t, name, dtype, shape, device):
     return ld
 
 
+def _like(x, shape):
+    """A contiguous tensor of x's type."""
+    return torch.empty_like(x) if x.is_contiguous() else x.new_empty(shape)
+
+
 def _work(nbytes, device):
     _raise(nbytes if nbytes < 0 else 0)
     return torch.empty(nbytes, dtype=torch.uint8, device=device) if nbytes else None
@@ -68,13 +108,14 @@ def _work(nbytes, device):
 
 def _gated_args(x, r, i, log_decay, shape):
     code = _act(x, "x")
-    dev = x.device
-    lds = [_row_stride(t, name, x.dtype, shape, dev) for t, name in ((x, "x"), (r, "r"), (i, "i"))]
+    dev, dtype, dim = x.device, x.dtype, shape[-1]
     if log_decay is None:
         raise ValueError("log_decay is required")
-    _check(log_decay, "log_decay", torch.float32, (shape[-1],), dev)
-    seqlen = shape[1] if len(shape) == 3 else 1
-    return _lib.GatedDims(shape[0], seqlen, shape[-1], *lds, code), dev
+    _check(log_decay, "log_decay", torch.float32, (dim,), dev)
+    return _lib.GatedDims(shape[0], shape[1] if len(shape) == 3 else 1, dim,
+                          _row_stride(x, "x", dtype, shape, dev),
+                          _row_stride(r, "r", dtype, shape, dev),
+                          _row_stride(i, "i", dtype, shape, dev), code), dev
 
 
 def _check_reset(reset, shape, dev):
@@ -89,7 +130,7 @@ def _check_ckpt(ckpt, dims, dev):
         return
     if ckpt.dtype != torch.float32 or ckpt.device != dev or not ckpt.is_contiguous():
         raise ValueError("ckpt must be a contiguous float32 tensor on the same device")
-    if ckpt.numel() * 4 < _lib.load().gated_ckpt_bytes(ctypes.byref(dims)):
+    if ckpt.numel() * 4 < _lib.load().gated_ckpt_bytes(byref(dims)):
         raise ValueError("ckpt is too small (use gated_ckpt_buffer)")
 
 
@@ -98,7 +139,7 @@ def gated_ckpt_buffer(x):
     state before every 16th step) of activations x [batch, L, dim]."""
     bsz, L, dim = x.shape
     dims = _lib.GatedDims(bsz, L, dim, dim, dim, dim, _act(x, "x"))
-    nbytes = _lib.load().gated_ckpt_bytes(ctypes.byref(dims))
+    nbytes = _lib.load().gated_ckpt_bytes(byref(dims))
     _raise(nbytes if nbytes < 0 else 0)
     return torch.empty(nbytes // 4, dtype=torch.float32, device=x.device)
 
@@ -120,24 +161,25 @@ def gated_scan_fwd(x, r, i, log_decay, reset=None, h0=None, return_last_state=Fa
     """
     if x.dim() != 3:
         raise ValueError("x must be [batch, L, dim]")
-    shape = tuple(x.shape)
+    shape = x.shape
     dims, dev = _gated_args(x, r, i, log_decay, shape)
     bsz, L, dim = shape
     _check_reset(reset, (bsz, L), dev)
     _check(h0, "h0", torch.float32, (bsz, dim), dev)
     _check_ckpt(ckpt, dims, dev)
     if out is None:
-        out = torch.empty(shape, dtype=x.dtype, device=dev)
-    _check(out, "out", x.dtype, shape, dev)
+        out = _like(x, shape)
+    else:
+        _check(out, "out", x.dtype, shape, dev)
     if return_last_state and last_state is None:
         last_state = torch.empty((bsz, dim), dtype=torch.float32, device=dev)
     _check(last_state, "last_state", torch.float32, (bsz, dim), dev)
     lib = _lib.load()
-    with torch.cuda.device(dev):
-        work = _work(lib.gated_scan_work_bytes(ctypes.byref(dims)), dev)
+    with _on(dev):
+        work = _work(lib.gated_scan_work_bytes(byref(dims)), dev)
         rc = lib.gated_scan_fwd(_ptr(x), _ptr(r), _ptr(i), _ptr(log_decay), _ptr(reset),
                                 _ptr(h0), _ptr(out), _ptr(last_state), _ptr(ckpt), _ptr(work),
-                                ctypes.byref(dims), _stream(dev))
+                                byref(dims), _stream(dev))
     _raise(rc)
     return (out, last_state) if return_last_state else out
 
@@ -154,7 +196,7 @@ def gated_scan_bwd(x, r, i, log_decay, dout, reset=None, h0=None, dlast=None, ck
     """
     if x.dim() != 3:
         raise ValueError("x must be [batch, L, dim]")
-    shape = tuple(x.shape)
+    shape = x.shape
     dims, dev = _gated_args(x, r, i, log_decay, shape)
     bsz, L, dim = shape
     _check_reset(reset, (bsz, L), dev)
@@ -164,18 +206,18 @@ def gated_scan_bwd(x, r, i, log_decay, dout, reset=None, h0=None, dlast=None, ck
     _check(dout, "dout", x.dtype, shape, dev)
     _check(dlast, "dlast", torch.float32, (bsz, dim), dev)
     _check_ckpt(ckpt, dims, dev)
-    g = {k: torch.empty(shape, dtype=x.dtype, device=dev) for k in ("dx", "dr", "di")}
+    g = {k: _like(x, shape) for k in ("dx", "dr", "di")}
     g["dlog_decay"] = torch.empty(dim, dtype=torch.float32, device=dev)
     if h0 is not None:
         g["dh0"] = torch.empty((bsz, dim), dtype=torch.float32, device=dev)
     lib = _lib.load()
-    with torch.cuda.device(dev):
-        work = _work(lib.gated_scan_bwd_work_bytes(ctypes.byref(dims), int(ckpt is not None)),
+    with _on(dev):
+        work = _work(lib.gated_scan_bwd_work_bytes(byref(dims), int(ckpt is not None)),
                      dev)
         rc = lib.gated_scan_bwd(_ptr(x), _ptr(r), _ptr(i), _ptr(log_decay), _ptr(reset),
                                 _ptr(h0), _ptr(dout), _ptr(dlast), _ptr(ckpt), _ptr(g["dx"]),
                                 _ptr(g["dr"]), _ptr(g["di"]), _ptr(g["dlog_decay"]),
-                                _ptr(g.get("dh0")), _ptr(work), ctypes.byref(dims),
+                                _ptr(g.get("dh0")), _ptr(work), byref(dims),
                                 _stream(dev))
     _raise(rc)
     return g
@@ -187,17 +229,18 @@ def gated_state_update(state, x, r, i, log_decay, out=None):
     [batch, dim] in x's dtype."""
     if x.dim() != 2:
         raise ValueError("x must be [batch, dim]")
-    shape = tuple(x.shape)
+    shape = x.shape
     dims, dev = _gated_args(x, r, i, log_decay, shape)
     if state is None:
         raise ValueError("state is required")
     _check(state, "state", torch.float32, shape, dev)
     if out is None:
-        out = torch.empty(shape, dtype=x.dtype, device=dev)
-    _check(out, "out", x.dtype, shape, dev)
-    with torch.cuda.device(dev):
+        out = _like(x, shape)
+    else:
+        _check(out, "out", x.dtype, shape, dev)
+    with _on(dev):
         rc = _lib.load().gated_state_update(_ptr(state), _ptr(x), _ptr(r), _ptr(i),
-                                            _ptr(log_decay), _ptr(out), ctypes.byref(dims),
+                                            _ptr(log_decay), _ptr(out), byref(dims),
                                             _stream(dev))
     _raise(rc)
     return out
@@ -213,7 +256,7 @@ def _rows(x, name):
 
 def _norm_args(x, weight, residual, residual_out):
     code, rows, dim = _rows(x, "x")
-    dev, shape = x.device, tuple(x.shape)
+    dev, shape = x.device, x.shape
     _check(x, "x", x.dtype, shape, dev)
     if weight is None:
         raise ValueError("weight is required")
@@ -225,8 +268,9 @@ def _norm_args(x, weight, residual, residual_out):
     rcode = _act(residual, "residual")
     _check(residual, "residual", residual.dtype, shape, dev)
     if residual_out is None:
-        residual_out = torch.empty(shape, dtype=residual.dtype, device=dev)
-    _check(residual_out, "residual_out", residual.dtype, shape, dev)
+        residual_out = torch.empty_like(residual)
+    else:
+        _check(residual_out, "residual_out", residual.dtype, shape, dev)
     return _lib.NormDims(rows, dim, code, rcode), dev, residual_out
 
 
@@ -241,17 +285,18 @@ def rms_norm_fwd(x, weight, residual=None, eps=1e-5, out=None, residual_out=None
     """
     dims, dev, residual_out = _norm_args(x, weight, residual, residual_out)
     if out is None:
-        out = torch.empty(x.shape, dtype=x.dtype, device=dev)
-    _check(out, "out", x.dtype, tuple(x.shape), dev)
-    with torch.cuda.device(dev):
+        out = torch.empty_like(x)
+    else:
+        _check(out, "out", x.dtype, x.shape, dev)
+    with _on(dev):
         rc = _lib.load().rms_norm_fwd(_ptr(x), _ptr(residual), _ptr(weight), eps, _ptr(out),
-                                      _ptr(residual_out), ctypes.byref(dims), _stream(dev))
+                                      _ptr(residual_out), byref(dims), _stream(dev))
     _raise(rc)
     return out if residual is None else (out, residual_out)
 
 
 def _fp8_outputs(x, rows, dim, dev):
-    q = torch.empty(x.shape, dtype=FP8, device=dev)
+    q = torch.empty_like(x, dtype=FP8)
     scale = torch.empty((-(-dim // FP8_GROUP), rows), dtype=torch.float32, device=dev)
     return q, scale
 
@@ -264,9 +309,9 @@ def rms_norm_fp8(x, weight, residual=None, eps=1e-5, residual_out=None):
     of 16."""
     dims, dev, residual_out = _norm_args(x, weight, residual, residual_out)
     q, scale = _fp8_outputs(x, dims.rows, dims.dim, dev)
-    with torch.cuda.device(dev):
+    with _on(dev):
         rc = _lib.load().rms_norm_fp8(_ptr(x), _ptr(residual), _ptr(weight), eps, _ptr(q),
-                                      _ptr(scale), _ptr(residual_out), ctypes.byref(dims),
+                                      _ptr(scale), _ptr(residual_out), byref(dims),
                                       _stream(dev))
     _raise(rc)
     return (q, scale) if residual is None else (q, scale, residual_out)
@@ -276,11 +321,11 @@ def fp8_quantize(x):
     """x [..., dim] (float32 or bfloat16) in 8 bits with a scale for every 128
     values of a row: (q, scale) as rms_norm_fp8 returns them."""
     code, rows, dim = _rows(x, "x")
-    _check(x, "x", x.dtype, tuple(x.shape), x.device)
+    _check(x, "x", x.dtype, x.shape, x.device)
     dims = _lib.NormDims(rows, dim, code, code)
     q, scale = _fp8_outputs(x, rows, dim, x.device)
-    with torch.cuda.device(x.device):
-        rc = _lib.load().fp8_quantize(_ptr(x), _ptr(q), _ptr(scale), ctypes.byref(dims),
+    with _on(x.device):
+        rc = _lib.load().fp8_quantize(_ptr(x), _ptr(q), _ptr(scale), byref(dims),
                                       _stream(x.device))
     _raise(rc)
     return q, scale
@@ -293,7 +338,7 @@ def rms_norm_bwd(dy, s, weight, eps=1e-5, dres=None):
     on the residual's own way.  Returns a dict: ds (s's dtype), the gradient of
     both x and residual, and dweight [dim] float32."""
     code, rows, dim = _rows(dy, "dy")
-    dev, shape = dy.device, tuple(dy.shape)
+    dev, shape = dy.device, dy.shape
     scode = _act(s, "s")
     _check(dy, "dy", dy.dtype, shape, dev)
     _check(s, "s", s.dtype, shape, dev)
@@ -302,13 +347,13 @@ def rms_norm_bwd(dy, s, weight, eps=1e-5, dres=None):
     _check(weight, "weight", torch.float32, (dim,), dev)
     _check(dres, "dres", s.dtype, shape, dev)
     dims = _lib.NormDims(rows, dim, code, scode)
-    g = dict(ds=torch.empty(shape, dtype=s.dtype, device=dev),
+    g = dict(ds=torch.empty_like(s),
              dweight=torch.empty(dim, dtype=torch.float32, device=dev))
     lib = _lib.load()
-    with torch.cuda.device(dev):
-        work = _work(lib.rms_norm_bwd_work_bytes(ctypes.byref(dims)), dev)
+    with _on(dev):
+        work = _work(lib.rms_norm_bwd_work_bytes(byref(dims)), dev)
         rc = lib.rms_norm_bwd(_ptr(dy), _ptr(s), _ptr(weight), eps, _ptr(dres), _ptr(g["ds"]),
-                              _ptr(g["dweight"]), _ptr(work), ctypes.byref(dims), _stream(dev))
+                              _ptr(g["dweight"]), _ptr(work), byref(dims), _stream(dev))
     _raise(rc)
     return g
 
@@ -325,7 +370,7 @@ def fp8_quantize_weight(w):
     q = torch.empty((n, k), dtype=FP8, device=w.device)
     scale = torch.empty((-(-n // FP8_GROUP), -(-k // FP8_GROUP)), dtype=torch.float32,
                         device=w.device)
-    with torch.cuda.device(w.device):
+    with _on(w.device):
         rc = _lib.load().fp8_quantize_weight(_ptr(w), code, n, k, _ptr(q), _ptr(scale),
                                              _stream(w.device))
     _raise(rc)
@@ -362,12 +407,13 @@ def fp8_linear(xq, x_scale, wq, w_scale, bias=None, out_dtype=torch.bfloat16, ou
     _check(bias, "bias", torch.float32, (n,), dev)
     if out is None:
         out = torch.empty(lead + (n,), dtype=out_dtype, device=dev)
-    _check(out, "out", out_dtype, lead + (n,), dev)
+    else:
+        _check(out, "out", out_dtype, lead + (n,), dev)
     dims = _lib.LinearDims(rows, n, k, _DTYPES[out_dtype])
     lib = _lib.load()
-    with torch.cuda.device(dev):
-        work = _work(lib.fp8_linear_work_bytes(ctypes.byref(dims)), dev)
+    with _on(dev):
+        work = _work(lib.fp8_linear_work_bytes(byref(dims)), dev)
         rc = lib.fp8_linear(_ptr(xq), _ptr(x_scale), _ptr(wq), _ptr(w_scale), _ptr(bias),
-                            _ptr(out), _ptr(work), ctypes.byref(dims), _stream(dev))
+                            _ptr(out), _ptr(work), byref(dims), _stream(dev))
     _raise(rc)
     return out
