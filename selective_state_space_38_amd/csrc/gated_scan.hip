@@ -151,6 +151,11 @@ struct Rows {
         w[j] = *p;
     }
   }
+  // Values computed from the rows so far are computed anew after this, not kept.
+  __device__ __forceinline__ void forget() {
+#pragma unroll
+    for (int j = 0; j < R; ++j) asm volatile("" : "+v"(w[j]));
+  }
   __device__ __forceinline__ float get(int j, int v) const {
     if constexpr (sizeof(T) == 4) return __uint_as_float(w[j]);
     return __uint_as_float(V == 2 && v == 1 ? (w[j] & 0xffff0000u) : (w[j] << 16));
@@ -407,7 +412,7 @@ __global__ __launch_bounds__(64 * kWaves, 4) void gated_bwd_kernel(GatedArgs p, 
     last[v] = p.dlast ? p.dlast[q.b * D + c + v] : 0.0f;
   }
   Rows<T, V, R> x, r, in, dout;
-  float rho[R][V], iota[R][V], a[R][V], beta[R][V], before[R][V], start[V];
+  float a[R][V], beta[R][V], before[R][V], start[V];
   float A[V], H[V];
 #pragma unroll
   for (int v = 0; v < V; ++v) {
@@ -428,8 +433,8 @@ __global__ __launch_bounds__(64 * kWaves, 4) void gated_bwd_kernel(GatedArgs p, 
     for (int j = 0; j < R; ++j)
 #pragma unroll
       for (int v = 0; v < V; ++v) {
-        gate(r.get(j, v), lam[v] * kLog2e, rho[j][v], a[j][v], beta[j][v]);
-        iota[j][v] = sigmoid_f32(in.get(j, v));
+        float rho;
+        gate(r.get(j, v), lam[v] * kLog2e, rho, a[j][v], beta[j][v]);
       }
   }
   // the states before each step, from the run's first
@@ -440,7 +445,7 @@ __global__ __launch_bounds__(64 * kWaves, 4) void gated_bwd_kernel(GatedArgs p, 
 #pragma unroll
       for (int v = 0; v < V; ++v) {
         before[j][v] = h[v];
-        const float ix = iota[j][v] * x.get(j, v);
+        const float ix = sigmoid_f32(in.get(j, v)) * x.get(j, v);
         h[v] = at_reset ? ix : fmaf(a[j][v], h[v], beta[j][v] * ix);
       }
     }
@@ -538,6 +543,8 @@ __global__ __launch_bounds__(64 * kWaves, 4) void gated_bwd_kernel(GatedArgs p, 
 #pragma unroll
   for (int v = 0; v < V; ++v) dlam[v] = 0.0f;
   if (n > 0) {
+    r.forget();
+    in.forget();
 #pragma unroll
     for (int j = R - 1; j >= 0; --j) {
       if (j >= n) continue;
@@ -545,7 +552,8 @@ __global__ __launch_bounds__(64 * kWaves, 4) void gated_bwd_kernel(GatedArgs p, 
       float dx[V], dr[V], di[V];
 #pragma unroll
       for (int v = 0; v < V; ++v) {
-        const float xt = x.get(j, v), io = iota[j][v], be = beta[j][v], al = a[j][v];
+        const float xt = x.get(j, v), be = beta[j][v], al = a[j][v];
+        const float rho = sigmoid_f32(r.get(j, v)), io = sigmoid_f32(in.get(j, v));
         const float gt = dout.get(j, v) + h[v];
         const float gi = gt * io;
         h[v] = at_reset ? 0.0f : al * gt;
@@ -553,8 +561,8 @@ __global__ __launch_bounds__(64 * kWaves, 4) void gated_bwd_kernel(GatedArgs p, 
         di[v] = dx[v] * xt * (1.0f - io);
         const float inv = be > 0.0f ? rcp_hw(be) : 0.0f;
         const float da = at_reset ? 0.0f : fmaf(h[v], before[j][v], -(al * al * inv) * (gi * xt));
-        const float dl = da * rho[j][v];
-        dr[v] = dl * lam[v] * (1.0f - rho[j][v]);
+        const float dl = da * rho;
+        dr[v] = dl * lam[v] * (1.0f - rho);
         dlam[v] += dl;
       }
       if (live) {
