@@ -3,6 +3,8 @@
 //   a = exp(log_decay rho), beta = sqrt(1 - a^2),
 //   h_t = a h_{t-1} + beta iota x_t.
 
+#include <stdlib.h>
+
 #include "layer_device.h"
 
 namespace ssm {
@@ -34,7 +36,7 @@ __device__ __forceinline__ void gate(float r, float lam2, float& rho, float& a, 
 
 // A wave owns V channels per lane (one dword of a row: 64 float32 or 128
 // bfloat16 channels, 256 bytes) and a run of kGatedRun steps; a workgroup is
-// up to kWaves consecutive runs of the same channels, a chunk of the sequence.
+// several consecutive runs of the same channels, a chunk of the sequence.
 // One pass over the run's gates and inputs leaves two numbers per step in
 // registers, the product A_j of a since the run's start and the state H_j from
 // zero; the runs' last ones meet in LDS, and once the state h before the run is
@@ -48,9 +50,10 @@ __device__ __forceinline__ void gate(float r, float lam2, float& rho, float& a, 
 // the aggregates since then forward, h = A h + H, in sequence order.  Since a
 // chunk's state is that same fold, where the walk stops does not change a bit
 // of the result.  Work is taken in ticket order, chunk by chunk, so a wait is
-// always for a workgroup that already runs.
-constexpr int kWaves = 8;
-constexpr int kChunk = kWaves * kGatedRun;
+// always for a workgroup that already runs.  (One counter hands out a ticket in
+// 13 ns; several, the channel blocks dealt to them, measured faster for chunks of
+// a few runs but slower for the larger ones, which are better than either.)
+constexpr int kMaxWaves = 16;
 
 // Record: state (code 1.0, sign clear) or aggregate (code -A, sign set); 0 is
 // empty.
@@ -146,7 +149,7 @@ struct Rows {
       const T* p = add_bytes(row, off);
       row += j + 1 < n ? ld : 0;
       if constexpr (sizeof(T) * V == 4)
-        w[j] = *reinterpret_cast<const uint32_t*>(p);
+        w[j] = __builtin_nontemporal_load(reinterpret_cast<const uint32_t*>(p));
       else
         w[j] = *p;
     }
@@ -167,7 +170,9 @@ __device__ __forceinline__ void store_row(void* base, int64_t elem, uint32_t off
                                           const float (&v)[V]) {
   T* p = add_bytes(static_cast<T*>(base) + elem, off);
   if constexpr (V == 2)
-    *reinterpret_cast<uint32_t*>(p) = pack_bf16x2(v[0], v[1]);
+    __builtin_nontemporal_store(pack_bf16x2(v[0], v[1]), reinterpret_cast<uint32_t*>(p));
+  else if constexpr (sizeof(T) == 4)
+    __builtin_nontemporal_store(v[0], p);
   else
     store_act(p, 0, v[0]);
 }
@@ -214,17 +219,79 @@ __device__ __forceinline__ uint32_t reset_bits(const GatedArgs& p, const Place& 
   return static_cast<uint32_t>(__ballot(on));
 }
 
+// What the waves of a workgroup share.
+template <int V>
+struct Shared {
+  float2 agg[kMaxWaves][64 * V];  // each run's product of a and state from zero
+  float carry[64 * V];
+  uint32_t cut[kMaxWaves];        // the run holds a reset
+  int ticket;
+};
+
+// h after the runs k0, k0 + dk, ... (count of them), from h before them.
+template <int V, bool RESET, typename S>
+__device__ __forceinline__ void fold_runs(const S& sh, int lane, int k0, int dk, int count,
+                                          float (&h)[V]) {
+  for (int k = k0; count > 0; --count, k += dk) {
+    const bool drop = RESET && sh.cut[k];
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      const float2 ag = sh.agg[k][lane * V + v];
+      h[v] = drop ? ag.y : fmaf(ag.x, h[v], ag.y);
+    }
+  }
+}
+
+// The state before a workgroup's chunk, into sh.carry: the chunk's aggregate
+// (runs from k0 in steps of dk) is published, the state before it found, and
+// the state after it published.  begin: the state before the sequence.  One
+// wave's work.
+template <int V, bool RESET>
+__device__ __forceinline__ void exchange(const GatedGrid& g, const Place& q, int spin_limit,
+                                         int lane, int k0, int dk, const float (&begin)[V],
+                                         Shared<V>& sh) {
+  uint64_t* rec = g.rec + (static_cast<int64_t>(q.chain) * g.chunks) * (64 * V) + lane * V;
+  uint64_t* own = rec + static_cast<int64_t>(q.chunk) * (64 * V);
+  const bool last = q.chunk == g.chunks - 1;
+  float A[V], H[V], h[V];
+  bool drop_any = false;
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    A[v] = 1.0f;
+    H[v] = 0.0f;
+    h[v] = begin[v];
+  }
+  for (int c = 0, k = k0; c < g.waves; ++c, k += dk) {
+    const bool drop = RESET && sh.cut[k];
+    drop_any = drop_any || drop;
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      const float2 ag = sh.agg[k][lane * V + v];
+      H[v] = drop ? ag.y : fmaf(ag.x, H[v], ag.y);
+      A[v] *= ag.x;
+    }
+  }
+  // after a reset the chunk's end does not depend on what came before
+  if (q.chunk && !last) put_records<V>(own, drop_any, A, H);
+  if (q.chunk) look_back<V>(rec, q.chunk - 1, spin_limit, h);
+  if (!last && !(drop_any && q.chunk)) {
+    float end[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) end[v] = drop_any ? H[v] : fmaf(A[v], h[v], H[v]);
+    put_records<V>(own, true, A, end);
+  }
+#pragma unroll
+  for (int v = 0; v < V; ++v) sh.carry[lane * V + v] = h[v];
+}
+
 template <typename T, int V, bool RESET, bool MULTI>
-__global__ __launch_bounds__(64 * kWaves) void gated_fwd_kernel(GatedArgs p, GatedGrid g) {
+__global__ __launch_bounds__(64 * kMaxWaves) void gated_fwd_kernel(GatedArgs p, GatedGrid g) {
   constexpr int R = kGatedRun;
-  __shared__ float2 s_agg[kWaves][64 * V];  // product of a, state from zero
-  __shared__ float s_carry[64 * V];
-  __shared__ uint32_t s_cut[kWaves];        // the run holds a reset
-  __shared__ int s_ticket;
+  __shared__ Shared<V> sh;
   const int lane = threadIdx.x & 63;
   const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int64_t D = p.dim, L = p.seqlen;
-  Place q = find_place<R, MULTI, false>(p, g, w, &s_ticket);
+  Place q = find_place<R, MULTI, false>(p, g, w, &sh.ticket);
   q.c0 *= 64 * V;
   const bool live = q.c0 + lane * V < D;
   const int64_t c = live ? q.c0 + lane * V : D - V;  // a dead lane repeats the last channels
@@ -290,70 +357,20 @@ __global__ __launch_bounds__(64 * kWaves) void gated_fwd_kernel(GatedArgs p, Gat
   const int W = g.waves;
   if (MULTI || W > 1) {
 #pragma unroll
-    for (int v = 0; v < V; ++v) s_agg[w][lane * V + v] = make_float2(A[R - 1][v], H[R - 1][v]);
-    if (RESET && lane == 0) s_cut[w] = cut;
+    for (int v = 0; v < V; ++v) sh.agg[w][lane * V + v] = make_float2(A[R - 1][v], H[R - 1][v]);
+    if (RESET && lane == 0) sh.cut[w] = cut;
     lds_barrier();
   }
-  // state after the runs before run `upto`, from state h before the chunk
-  auto fold = [&](int upto, float (&h)[V]) {
-    for (int k = 0; k < upto; ++k) {
-      const bool drop = RESET && s_cut[k];
-#pragma unroll
-      for (int v = 0; v < V; ++v) {
-        const float2 ag = s_agg[k][lane * V + v];
-        h[v] = drop ? ag.y : fmaf(ag.x, h[v], ag.y);
-      }
-    }
-  };
   float h[V];
+#pragma unroll
+  for (int v = 0; v < V; ++v) h[v] = first[v];
   if (MULTI) {
-    if (w == 0) {
-      uint64_t* rec = g.rec + (static_cast<int64_t>(q.chain) * g.chunks) * (64 * V) + lane * V;
-      uint64_t* own = rec + static_cast<int64_t>(q.chunk) * (64 * V);
-      float cA[V], cH[V];
-      bool drop_any = false;
-#pragma unroll
-      for (int v = 0; v < V; ++v) {
-        cA[v] = 1.0f;
-        cH[v] = 0.0f;
-      }
-      for (int k = 0; k < W; ++k) {
-        const bool drop = RESET && s_cut[k];
-        drop_any = drop_any || drop;
-#pragma unroll
-        for (int v = 0; v < V; ++v) {
-          const float2 ag = s_agg[k][lane * V + v];
-          cH[v] = drop ? ag.y : fmaf(ag.x, cH[v], ag.y);
-          cA[v] *= ag.x;
-        }
-      }
-      const bool last = q.chunk == g.chunks - 1;
-      if (q.chunk == 0) {
-#pragma unroll
-        for (int v = 0; v < V; ++v) h[v] = first[v];
-      } else {
-        // after a reset the chunk's end does not depend on what came before
-        if (!last) put_records<V>(own, drop_any, cA, cH);
-        look_back<V>(rec, q.chunk - 1, p.spin_limit, h);
-      }
-      if (!last && !(drop_any && q.chunk)) {
-        float end[V];
-#pragma unroll
-        for (int v = 0; v < V; ++v) end[v] = drop_any ? cH[v] : fmaf(cA[v], h[v], cH[v]);
-        put_records<V>(own, true, cA, end);
-      }
-#pragma unroll
-      for (int v = 0; v < V; ++v) s_carry[lane * V + v] = h[v];
-    }
+    if (w == 0) exchange<V, RESET>(g, q, p.spin_limit, lane, 0, 1, first, sh);
     lds_barrier();
 #pragma unroll
-    for (int v = 0; v < V; ++v) h[v] = s_carry[lane * V + v];
-    fold(w, h);
-  } else {
-#pragma unroll
-    for (int v = 0; v < V; ++v) h[v] = first[v];
-    if (W > 1) fold(w, h);
+    for (int v = 0; v < V; ++v) h[v] = sh.carry[lane * V + v];
   }
+  fold_runs<V, RESET>(sh, lane, 0, 1, w, h);
   if (n <= 0 || !live) return;
   if (p.ckpt) {
     float* ck = p.ckpt + (q.b * div_up64(L, R) + q.t0 / R) * D + c;
@@ -384,20 +401,16 @@ __global__ __launch_bounds__(64 * kWaves) void gated_fwd_kernel(GatedArgs p, Gat
 // through their even neighbour's aggregate.  c runs through the chunk and over
 // the chunks as h does forward (chunks are taken from the sequence's end).
 constexpr int kBwdRun = kGatedRun / 2;
-constexpr int kBwdChunk = kWaves * kBwdRun;
 
 template <typename T, int V, bool RESET, bool MULTI>
-__global__ __launch_bounds__(64 * kWaves, 4) void gated_bwd_kernel(GatedArgs p, GatedGrid g) {
+__global__ __launch_bounds__(64 * kMaxWaves) void gated_bwd_kernel(GatedArgs p, GatedGrid g) {
   constexpr int R = kBwdRun;
-  __shared__ float2 s_agg[kWaves][64 * V];
-  __shared__ float s_carry[64 * V];
-  __shared__ float s_mid[kWaves / 2][64 * V];  // state after an even wave's run
-  __shared__ uint32_t s_cut[kWaves];
-  __shared__ int s_ticket;
+  __shared__ Shared<V> sh;
+  __shared__ float s_mid[kMaxWaves / 2][64 * V];  // state after an even wave's run
   const int lane = threadIdx.x & 63;
   const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int64_t D = p.dim, L = p.seqlen;
-  Place q = find_place<R, MULTI, true>(p, g, w, &s_ticket);
+  Place q = find_place<R, MULTI, true>(p, g, w, &sh.ticket);
   q.c0 *= 64 * V;
   const bool live = q.c0 + lane * V < D;
   const int64_t c = live ? q.c0 + lane * V : D - V;
@@ -476,69 +489,20 @@ __global__ __launch_bounds__(64 * kWaves, 4) void gated_bwd_kernel(GatedArgs p, 
   }
   if (MULTI || W > 1) {
 #pragma unroll
-    for (int v = 0; v < V; ++v) s_agg[w][lane * V + v] = make_float2(A[v], H[v]);
-    if (RESET && lane == 0) s_cut[w] = cut;
+    for (int v = 0; v < V; ++v) sh.agg[w][lane * V + v] = make_float2(A[v], H[v]);
+    if (RESET && lane == 0) sh.cut[w] = cut;
     lds_barrier();
   }
-  // c before the runs after run `from`, from c after the chunk
-  auto fold = [&](int from, float (&h)[V]) {
-    for (int k = W - 1; k > from; --k) {
-      const bool drop = RESET && s_cut[k];
-#pragma unroll
-      for (int v = 0; v < V; ++v) {
-        const float2 ag = s_agg[k][lane * V + v];
-        h[v] = drop ? ag.y : fmaf(ag.x, h[v], ag.y);
-      }
-    }
-  };
   float h[V];
+#pragma unroll
+  for (int v = 0; v < V; ++v) h[v] = last[v];
   if (MULTI) {
-    if (w == 0) {
-      uint64_t* rec = g.rec + (static_cast<int64_t>(q.chain) * g.chunks) * (64 * V) + lane * V;
-      uint64_t* own = rec + static_cast<int64_t>(q.chunk) * (64 * V);
-      float cA[V], cH[V];
-      bool drop_any = false;
-#pragma unroll
-      for (int v = 0; v < V; ++v) {
-        cA[v] = 1.0f;
-        cH[v] = 0.0f;
-      }
-      for (int k = W - 1; k >= 0; --k) {
-        const bool drop = RESET && s_cut[k];
-        drop_any = drop_any || drop;
-#pragma unroll
-        for (int v = 0; v < V; ++v) {
-          const float2 ag = s_agg[k][lane * V + v];
-          cH[v] = drop ? ag.y : fmaf(ag.x, cH[v], ag.y);
-          cA[v] *= ag.x;
-        }
-      }
-      const bool final_chunk = q.chunk == g.chunks - 1;  // the sequence's first
-      if (q.chunk == 0) {
-#pragma unroll
-        for (int v = 0; v < V; ++v) h[v] = last[v];
-      } else {
-        if (!final_chunk) put_records<V>(own, drop_any, cA, cH);
-        look_back<V>(rec, q.chunk - 1, p.spin_limit, h);
-      }
-      if (!final_chunk && !(drop_any && q.chunk)) {
-        float end[V];
-#pragma unroll
-        for (int v = 0; v < V; ++v) end[v] = drop_any ? cH[v] : fmaf(cA[v], h[v], cH[v]);
-        put_records<V>(own, true, cA, end);
-      }
-#pragma unroll
-      for (int v = 0; v < V; ++v) s_carry[lane * V + v] = h[v];
-    }
+    if (w == 0) exchange<V, RESET>(g, q, p.spin_limit, lane, W - 1, -1, last, sh);
     lds_barrier();
 #pragma unroll
-    for (int v = 0; v < V; ++v) h[v] = s_carry[lane * V + v];
-    fold(w, h);
-  } else {
-#pragma unroll
-    for (int v = 0; v < V; ++v) h[v] = last[v];
-    if (W > 1) fold(w, h);
+    for (int v = 0; v < V; ++v) h[v] = sh.carry[lane * V + v];
   }
+  fold_runs<V, RESET>(sh, lane, W - 1, -1, W - 1 - w, h);
   float dlam[V];
 #pragma unroll
   for (int v = 0; v < V; ++v) dlam[v] = 0.0f;
@@ -577,15 +541,15 @@ __global__ __launch_bounds__(64 * kWaves, 4) void gated_bwd_kernel(GatedArgs p, 
     }
   }
   // the workgroup's dlog_decay, run by run
-  lds_barrier();  // s_agg was read by every wave's fold
+  lds_barrier();  // the aggregates were read by every wave's fold
 #pragma unroll
-  for (int v = 0; v < V; ++v) s_agg[w][lane * V + v].x = dlam[v];
+  for (int v = 0; v < V; ++v) sh.agg[w][lane * V + v].x = dlam[v];
   lds_barrier();
   if (w == 0 && live) {
 #pragma unroll
     for (int v = 0; v < V; ++v) {
       float sum = 0.0f;
-      for (int k = 0; k < W; ++k) sum += s_agg[k][lane * V + v].x;
+      for (int k = 0; k < W; ++k) sum += sh.agg[k][lane * V + v].x;
       g.part[(q.b * g.chunks + q.chunk) * D + c + v] = sum;
     }
   }
@@ -645,41 +609,80 @@ void launch_column_sum(const float* part, int64_t rows, int64_t dim, float* out,
   column_sum_kernel<<<blocks_of(dim, 64), 1024, 0, stream>>>(part, rows, dim, out);
 }
 
-// Channels per lane: two where rows can be moved in whole dwords of bfloat16
-// (an even dim and row strides, 4-byte aligned rows), else one.
-static int channels_per_lane(const GatedArgs& a) {
-  if (a.dtype == 0) return 1;
-  if ((a.dim | a.ld_x | a.ld_r | a.ld_i) & 1) return 1;
+// Whether rows can be moved in whole dwords of two bfloat16: an even dim and row
+// strides, 4-byte aligned rows.
+static bool pairs_of_channels(const GatedArgs& a) {
+  if (a.dtype == 0) return false;
+  if ((a.dim | a.ld_x | a.ld_r | a.ld_i) & 1) return false;
   for (const void* q : {a.x, a.r, a.i, static_cast<const void*>(a.out), a.dout,
                         static_cast<const void*>(a.dx), static_cast<const void*>(a.dr),
                         static_cast<const void*>(a.di)})
-    if (reinterpret_cast<uintptr_t>(q) & 3) return 1;
-  return 2;
+    if (reinterpret_cast<uintptr_t>(q) & 3) return false;
+  return true;
 }
 
-// Scratch of a pass over chunks: a ticket (16 bytes) and the records, for the
-// wider of the two channel layouts' padding.
-static int64_t record_bytes(int64_t batch, int64_t seqlen, int64_t dim, int chunk) {
-  const int64_t chunks = div_up64(seqlen, chunk);
-  return chunks <= 1 ? 0 : 16 + batch * chunks * div_up64(dim, 128) * 128 * 8;
+// Shape of a pass in runs of `run` steps: channels per lane, waves per
+// workgroup, channel blocks over all batch rows, chunks per sequence.
+struct Cut {
+  int v, waves;
+  int64_t chains, chunks;
+};
+// Two channels per lane where they can be and there is work for every CU all the
+// same.  Eight waves a workgroup; sixteen where a sequence has many chunks and
+// few channel blocks, since what bounds it then is the hop from chunk to chunk
+// (70 ns each; a million steps of 64 bfloat16 channels: 261 us so, 448 with two
+// channels per lane, 478 with eight waves, 856 with both; of 256 float32
+// channels 764 us against 912), while more blocks run faster with two
+// workgroups on a CU (2.8B-shaped layer 284 us against 334, four waves 304).
+// SSM_FORCE_GATED_WAVES overrides (tests, tuning).
+static Cut cut_of(bool pairs, int64_t batch, int64_t seqlen, int64_t dim, int run) {
+  Cut c;
+  const int64_t chunks = div_up64(seqlen, 8 * run);
+  c.v = pairs && batch * div_up64(dim, 64) > 2 && batch * div_up64(dim, 128) * chunks >= 256 ? 2 : 1;
+  c.chains = batch * div_up64(dim, 64 * c.v);
+  c.waves = c.chains <= 8 && c.chains * chunks >= 512 ? 16 : 8;
+  const char* force = getenv("SSM_FORCE_GATED_WAVES");
+  if (force && *force) {
+    const int w = atoi(force) & ~1;  // the backward's waves work in pairs
+    c.waves = w < 2 ? 2 : (w > kMaxWaves ? kMaxWaves : w);
+  }
+  c.chunks = div_up64(seqlen, c.waves * run);
+  if (c.chunks == 1) c.waves = static_cast<int>(div_up64(seqlen, run));
+  return c;
 }
 
-int64_t gated_fwd_work(int, int64_t batch, int64_t seqlen, int64_t dim) {
-  return record_bytes(batch, seqlen, dim, kChunk);
-}
-int64_t gated_bwd_work(int, int64_t batch, int64_t seqlen, int64_t dim) {
-  return record_bytes(batch, seqlen, dim, kBwdChunk) +
-         batch * div_up64(seqlen, kBwdChunk) * dim * 4;
+// Scratch of a pass over chunks: a ticket (16 bytes) and the records.
+static int64_t record_bytes(const Cut& c) {
+  return c.chunks <= 1 ? 0 : 16 + c.chains * c.chunks * c.v * 64 * 8;
 }
 
-static GatedGrid grid_of(const GatedArgs& a, int v, int run, hipStream_t stream) {
-  const int chunk = kWaves * run;
+// The query does not see the tensors' alignment: the larger of the two layouts.
+static int64_t work_bytes(int dtype, int64_t batch, int64_t seqlen, int64_t dim, int run,
+                          bool parts) {
+  int64_t most = 0;
+  for (int pairs = 0; pairs <= (dtype != 0); ++pairs) {
+    const Cut c = cut_of(pairs != 0, batch, seqlen, dim, run);
+    const int64_t bytes = record_bytes(c) + (parts ? batch * c.chunks * dim * 4 : 0);
+    most = bytes > most ? bytes : most;
+  }
+  return most;
+}
+int64_t gated_fwd_work(int dtype, int64_t batch, int64_t seqlen, int64_t dim) {
+  return work_bytes(dtype, batch, seqlen, dim, kGatedRun, false);
+}
+int64_t gated_bwd_work(int dtype, int64_t batch, int64_t seqlen, int64_t dim) {
+  return work_bytes(dtype, batch, seqlen, dim, kBwdRun, true);
+}
+
+static GatedGrid grid_of(const GatedArgs& a, int run, int* v, hipStream_t stream) {
+  const Cut c = cut_of(pairs_of_channels(a), a.batch, a.seqlen, a.dim, run);
   GatedGrid g = {};
-  g.n_cblk = static_cast<int>(div_up64(a.dim, 64 * v));
-  g.chains = static_cast<int>(a.batch) * g.n_cblk;
-  g.chunks = static_cast<int>(div_up64(a.seqlen, chunk));
-  g.waves = g.chunks > 1 ? kWaves : static_cast<int>(div_up64(a.seqlen, run));
-  const int64_t bytes = record_bytes(a.batch, a.seqlen, a.dim, chunk);
+  g.n_cblk = static_cast<int>(div_up64(a.dim, 64 * c.v));
+  g.chains = static_cast<int>(c.chains);
+  g.chunks = static_cast<int>(c.chunks);
+  g.waves = c.waves;
+  *v = c.v;
+  const int64_t bytes = record_bytes(c);
   if (bytes) {
     g.ticket = static_cast<int*>(a.work);
     g.rec = reinterpret_cast<uint64_t*>(static_cast<char*>(a.work) + 16);
@@ -716,15 +719,15 @@ static GatedGrid grid_of(const GatedArgs& a, int v, int run, hipStream_t stream)
   }
 
 hipError_t launch_gated_fwd(const GatedArgs& a, hipStream_t stream) {
-  const int v = channels_per_lane(a);
-  const GatedGrid g = grid_of(a, v, kGatedRun, stream);
+  int v;
+  const GatedGrid g = grid_of(a, kGatedRun, &v, stream);
   SSM_LAUNCH_GATED(gated_fwd_kernel);
   return hipGetLastError();
 }
 
 hipError_t launch_gated_bwd(const GatedArgs& a, hipStream_t stream) {
-  const int v = channels_per_lane(a);
-  const GatedGrid g = grid_of(a, v, kBwdRun, stream);
+  int v;
+  const GatedGrid g = grid_of(a, kBwdRun, &v, stream);
   SSM_LAUNCH_GATED(gated_bwd_kernel);
   launch_column_sum(g.part, a.batch * g.chunks, a.dim, a.dlog_decay, stream);
   return hipGetLastError();
