@@ -150,8 +150,15 @@ __global__ __launch_bounds__(1024) void fp8_stream_kernel(LinearArgs p) {
 typedef const __attribute__((address_space(1))) void* global_ptr;
 typedef __attribute__((address_space(3))) void* lds_ptr;
 
-__device__ __forceinline__ int key_w(int row) { return (row & 3) | ((row >> 1) & 4); }
-__device__ __forceinline__ int key_x(int row) { return row & 7; }
+// A 16-byte read is served 16 lanes at a time from 64 banks, two rows' worth, so
+// the 8 even rows of a tile and the 8 odd ones each have keys of their own; and
+// the lanes served together can belong to two neighbouring quads (whose chunks
+// differ by 2), the middle 8 rows to one and the outer 8 to the other, so the
+// middle rows' keys are 0 .. 3 and the outer ones' 4 .. 7, sets that stay apart
+// under an exclusive or of either.  pair: half the row's number in the tile.
+__device__ __forceinline__ int key_of(int pair) { return ((pair + 2) & 7) ^ 4; }
+__device__ __forceinline__ int key_w(int row) { return key_of(((row >> 2) & 6) | ((row >> 1) & 1)); }
+__device__ __forceinline__ int key_x(int row) { return key_of((row >> 1) & 7); }
 
 // What a lane loads for a place past a row's end.
 __device__ const uint4 g_zeros = {0, 0, 0, 0};
