@@ -223,6 +223,20 @@ __device__ __forceinline__ void tile_of(int64_t tiles_m, int64_t tiles_n, int64_
   *tn = in / high;
 }
 
+template <typename T>
+__device__ __forceinline__ void store8_stream(T* p, const float (&v)[8]) {
+  typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+  if constexpr (sizeof(T) == 2) {
+    const u32x4 t = {pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
+                     pack_bf16x2(v[6], v[7])};
+    __builtin_nontemporal_store(t, reinterpret_cast<u32x4*>(p));
+  } else {
+    const f32x4 lo = {v[0], v[1], v[2], v[3]}, hi = {v[4], v[5], v[6], v[7]};
+    __builtin_nontemporal_store(lo, reinterpret_cast<f32x4*>(p));
+    __builtin_nontemporal_store(hi, reinterpret_cast<f32x4*>(p) + 1);
+  }
+}
+
 template <typename T, int BN, int BM, int WN, int WM>
 __global__ __launch_bounds__(64 * WN * WM) void fp8_tile_kernel(LinearArgs p) {
   constexpr int WAVES = WN * WM, NT = BN / WN / 16, MT = BM / WM / 16;
@@ -378,7 +392,11 @@ __global__ __launch_bounds__(64 * WN * WM) void fp8_tile_kernel(LinearArgs p) {
         float v[8];
 #pragma unroll
         for (int e = 0; e < 8; ++e) v[e] = acc[t * 2 + e / 4][m][e % 4] + bias[e];
-        store_run<O, 8>(out + tok * p.n + n, v, whole, last);
+        // the largest tiles' outputs exceed the caches: they stream past them
+        if (BN * BM == 65536 && whole)
+          store8_stream(out + tok * p.n + n, v);
+        else
+          store_run<O, 8>(out + tok * p.n + n, v, whole, last);
       }
     }
   };
