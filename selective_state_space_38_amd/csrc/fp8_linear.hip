@@ -223,20 +223,6 @@ __device__ __forceinline__ void tile_of(int64_t tiles_m, int64_t tiles_n, int64_
   *tn = in / high;
 }
 
-template <typename T>
-__device__ __forceinline__ void store8_stream(T* p, const float (&v)[8]) {
-  typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
-  if constexpr (sizeof(T) == 2) {
-    const u32x4 t = {pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
-                     pack_bf16x2(v[6], v[7])};
-    __builtin_nontemporal_store(t, reinterpret_cast<u32x4*>(p));
-  } else {
-    const f32x4 lo = {v[0], v[1], v[2], v[3]}, hi = {v[4], v[5], v[6], v[7]};
-    __builtin_nontemporal_store(lo, reinterpret_cast<f32x4*>(p));
-    __builtin_nontemporal_store(hi, reinterpret_cast<f32x4*>(p) + 1);
-  }
-}
-
 template <typename T, int BN, int BM, int WN, int WM>
 __global__ __launch_bounds__(64 * WN * WM) void fp8_tile_kernel(LinearArgs p) {
   constexpr int WAVES = WN * WM, NT = BN / WN / 16, MT = BM / WM / 16;
@@ -374,7 +360,6 @@ __global__ __launch_bounds__(64 * WN * WM) void fp8_tile_kernel(LinearArgs p) {
   // 8 consecutive outputs of a token at a time
   auto store = [&](auto* out, const float* bias_of) {
     using O = typename std::remove_reference<decltype(*out)>::type;
-    const bool whole = p.n % 8 == 0 && reinterpret_cast<uintptr_t>(out) % 16 == 0;
 #pragma unroll
     for (int t = 0; t < NT / 2; ++t) {
       const int64_t n = nw + t * 32 + quad * 8;
@@ -393,10 +378,7 @@ __global__ __launch_bounds__(64 * WN * WM) void fp8_tile_kernel(LinearArgs p) {
 #pragma unroll
         for (int e = 0; e < 8; ++e) v[e] = acc[t * 2 + e / 4][m][e % 4] + bias[e];
         // the largest tiles' outputs exceed the caches: they stream past them
-        if (BN * BM == 65536 && whole)
-          store8_stream(out + tok * p.n + n, v);
-        else
-          store_run<O, 8>(out + tok * p.n + n, v, whole, last);
+        store8<O, BN * BM == 65536>(out + tok * p.n + n, v, last);
       }
     }
   };
@@ -477,8 +459,9 @@ static int forced(const char* name) {
 // 256, 640 65 against 79, 320 77 against 74).
 //
 // 64 x 64 tiles may split the inputs into parts.  Measured: about 0.42 us a
-// block, and 2 us for the join plus its traffic, written and read at 2.5 TB/s;
-// the least sum of the two is taken.  SSM_FORCE_LINEAR_SHAPE and _PARTS override
+// block; for the join 2 us, its traffic, written and read at 2.5 TB/s, and its
+// launch on the host, which takes another 2 from a caller that launches one call
+// after the other; the least sum of the two is taken.  SSM_FORCE_LINEAR_SHAPE and _PARTS override
 // (tests, tuning).
 static Plan plan_of(int dtype, int64_t rows, int64_t n, int64_t k) {
   Plan q = {kStream, 1};
@@ -495,7 +478,7 @@ static Plan plan_of(int dtype, int64_t rows, int64_t n, int64_t k) {
       double best = 0.0;
       for (int t = 1; t <= 8 && t <= groups; ++t) {
         const double blocks = static_cast<double>(div_up64(groups, t)) * div_up64(tiles(64) * t, 512);
-        const double us = 0.42 * blocks + (t > 1 ? 2.0 + 8e-6 / 2.5 * rows * n * t : 0.0);
+        const double us = 0.42 * blocks + (t > 1 ? 4.0 + 8e-6 / 2.5 * rows * n * t : 0.0);
         if (t == 1 || us < best) {
           best = us;
           q.parts = t;

@@ -149,7 +149,7 @@ struct Rows {
       const T* p = add_bytes(row, off);
       row += j + 1 < n ? ld : 0;
       if constexpr (sizeof(T) * V == 4)
-        w[j] = __builtin_nontemporal_load(reinterpret_cast<const uint32_t*>(p));
+        w[j] = __builtin_nontemporal_load(reinterpret_cast<const u32_any*>(p));
       else
         w[j] = *p;
     }
@@ -170,7 +170,7 @@ __device__ __forceinline__ void store_row(void* base, int64_t elem, uint32_t off
                                           const float (&v)[V]) {
   T* p = add_bytes(static_cast<T*>(base) + elem, off);
   if constexpr (V == 2)
-    __builtin_nontemporal_store(pack_bf16x2(v[0], v[1]), reinterpret_cast<uint32_t*>(p));
+    __builtin_nontemporal_store(pack_bf16x2(v[0], v[1]), reinterpret_cast<u32_any*>(p));
   else if constexpr (sizeof(T) == 4)
     __builtin_nontemporal_store(v[0], p);
   else
@@ -294,8 +294,11 @@ __global__ __launch_bounds__(64 * kMaxWaves) void gated_fwd_kernel(GatedArgs p, 
   Place q = find_place<R, MULTI, false>(p, g, w, &sh.ticket);
   q.c0 *= 64 * V;
   const bool live = q.c0 + lane * V < D;
-  const int64_t c = live ? q.c0 + lane * V : D - V;  // a dead lane repeats the last channels
-  const uint32_t off = static_cast<uint32_t>((c - q.c0) * static_cast<int64_t>(sizeof(T)));
+  // a dead lane repeats the last channels, and so does the half-filled last lane
+  // of an odd dim: it computes and stores what its neighbour does
+  const int64_t c = q.c0 + lane * V <= D - V ? q.c0 + lane * V : D - V;
+  const int64_t cb = q.c0 <= D - V ? q.c0 : D - V;  // where the block's rows are addressed from
+  const uint32_t off = static_cast<uint32_t>((c - cb) * static_cast<int64_t>(sizeof(T)));
   const int n = q.n;
 
   float lam2[V];
@@ -310,9 +313,9 @@ __global__ __launch_bounds__(64 * kMaxWaves) void gated_fwd_kernel(GatedArgs p, 
   if (n > 0) {
     const int64_t row = q.b * L + q.t0;
     Rows<T, V, R> x, r, in;
-    r.load(p.r, row * p.ld_r + q.c0, p.ld_r, off, n);
-    in.load(p.i, row * p.ld_i + q.c0, p.ld_i, off, n);
-    x.load(p.x, row * p.ld_x + q.c0, p.ld_x, off, n);
+    r.load(p.r, row * p.ld_r + cb, p.ld_r, off, n);
+    in.load(p.i, row * p.ld_i + cb, p.ld_i, off, n);
+    x.load(p.x, row * p.ld_x + cb, p.ld_x, off, n);
     if (RESET) cut = reset_bits(p, q, lane);
 #pragma unroll
     for (int j = 0; j < R; ++j) {
@@ -385,7 +388,7 @@ __global__ __launch_bounds__(64 * kMaxWaves) void gated_fwd_kernel(GatedArgs p, 
     const bool since = RESET && (cut & ((2u << j) - 1)) != 0;
 #pragma unroll
     for (int v = 0; v < V; ++v) o[v] = since ? H[j][v] : fmaf(A[j][v], h[v], H[j][v]);
-    if (p.out && j < n) store_row<T, V>(p.out, (row + j) * D + q.c0, off, o);
+    if (p.out && j < n) store_row<T, V>(p.out, (row + j) * D + cb, off, o);
   }
   if (p.last_state && q.t0 + n == L) {
 #pragma unroll
@@ -413,8 +416,9 @@ __global__ __launch_bounds__(64 * kMaxWaves) void gated_bwd_kernel(GatedArgs p, 
   Place q = find_place<R, MULTI, true>(p, g, w, &sh.ticket);
   q.c0 *= 64 * V;
   const bool live = q.c0 + lane * V < D;
-  const int64_t c = live ? q.c0 + lane * V : D - V;
-  const uint32_t off = static_cast<uint32_t>((c - q.c0) * static_cast<int64_t>(sizeof(T)));
+  const int64_t c = q.c0 + lane * V <= D - V ? q.c0 + lane * V : D - V;
+  const int64_t cb = q.c0 <= D - V ? q.c0 : D - V;  // where the block's rows are addressed from
+  const uint32_t off = static_cast<uint32_t>((c - cb) * static_cast<int64_t>(sizeof(T)));
   const int n = q.n;
   const int64_t row = q.b * L + q.t0;
 
@@ -434,10 +438,10 @@ __global__ __launch_bounds__(64 * kMaxWaves) void gated_bwd_kernel(GatedArgs p, 
   }
   uint32_t cut = 0;
   if (n > 0) {
-    r.load(p.r, row * p.ld_r + q.c0, p.ld_r, off, n);
-    in.load(p.i, row * p.ld_i + q.c0, p.ld_i, off, n);
-    x.load(p.x, row * p.ld_x + q.c0, p.ld_x, off, n);
-    dout.load(p.dout, row * D + q.c0, D, off, n);
+    r.load(p.r, row * p.ld_r + cb, p.ld_r, off, n);
+    in.load(p.i, row * p.ld_i + cb, p.ld_i, off, n);
+    x.load(p.x, row * p.ld_x + cb, p.ld_x, off, n);
+    dout.load(p.dout, row * D + cb, D, off, n);
     if (RESET) cut = reset_bits(p, q, lane);
 #pragma unroll
     for (int v = 0; v < V; ++v)
@@ -530,9 +534,9 @@ __global__ __launch_bounds__(64 * kMaxWaves) void gated_bwd_kernel(GatedArgs p, 
         dlam[v] += dl;
       }
       if (live) {
-        store_row<T, V>(p.dx, (row + j) * D + q.c0, off, dx);
-        store_row<T, V>(p.dr, (row + j) * D + q.c0, off, dr);
-        store_row<T, V>(p.di, (row + j) * D + q.c0, off, di);
+        store_row<T, V>(p.dx, (row + j) * D + cb, off, dx);
+        store_row<T, V>(p.dr, (row + j) * D + cb, off, dr);
+        store_row<T, V>(p.di, (row + j) * D + cb, off, di);
       }
     }
     if (p.dh0 && q.t0 == 0 && live) {
@@ -609,36 +613,24 @@ void launch_column_sum(const float* part, int64_t rows, int64_t dim, float* out,
   column_sum_kernel<<<blocks_of(dim, 64), 1024, 0, stream>>>(part, rows, dim, out);
 }
 
-// Whether rows can be moved in whole dwords of two bfloat16: an even dim and row
-// strides, 4-byte aligned rows.
-static bool pairs_of_channels(const GatedArgs& a) {
-  if (a.dtype == 0) return false;
-  if ((a.dim | a.ld_x | a.ld_r | a.ld_i) & 1) return false;
-  for (const void* q : {a.x, a.r, a.i, static_cast<const void*>(a.out), a.dout,
-                        static_cast<const void*>(a.dx), static_cast<const void*>(a.dr),
-                        static_cast<const void*>(a.di)})
-    if (reinterpret_cast<uintptr_t>(q) & 3) return false;
-  return true;
-}
-
 // Shape of a pass in runs of `run` steps: channels per lane, waves per
 // workgroup, channel blocks over all batch rows, chunks per sequence.
 struct Cut {
   int v, waves;
   int64_t chains, chunks;
 };
-// Two channels per lane where they can be and there is work for every CU all the
-// same.  Eight waves a workgroup; sixteen where a sequence has many chunks and
+// Two bfloat16 channels per lane where there is work for every CU all the same.  Eight waves a workgroup; sixteen where a sequence has many chunks and
 // few channel blocks, since what bounds it then is the hop from chunk to chunk
 // (70 ns each; a million steps of 64 bfloat16 channels: 261 us so, 448 with two
 // channels per lane, 478 with eight waves, 856 with both; of 256 float32
 // channels 764 us against 912), while more blocks run faster with two
 // workgroups on a CU (2.8B-shaped layer 284 us against 334, four waves 304).
 // SSM_FORCE_GATED_WAVES overrides (tests, tuning).
-static Cut cut_of(bool pairs, int64_t batch, int64_t seqlen, int64_t dim, int run) {
+static Cut cut_of(int dtype, int64_t batch, int64_t seqlen, int64_t dim, int run) {
   Cut c;
   const int64_t chunks = div_up64(seqlen, 8 * run);
-  c.v = pairs && batch * div_up64(dim, 64) > 2 && batch * div_up64(dim, 128) * chunks >= 256 ? 2 : 1;
+  const bool pairs = dtype != 0 && batch * div_up64(dim, 64) > 2;
+  c.v = pairs && dim > 1 && batch * div_up64(dim, 128) * chunks >= 256 ? 2 : 1;
   c.chains = batch * div_up64(dim, 64 * c.v);
   c.waves = c.chains <= 8 && c.chains * chunks >= 512 ? 16 : 8;
   const char* force = getenv("SSM_FORCE_GATED_WAVES");
@@ -647,7 +639,11 @@ static Cut cut_of(bool pairs, int64_t batch, int64_t seqlen, int64_t dim, int ru
     c.waves = w < 2 ? 2 : (w > kMaxWaves ? kMaxWaves : w);
   }
   c.chunks = div_up64(seqlen, c.waves * run);
-  if (c.chunks == 1) c.waves = static_cast<int>(div_up64(seqlen, run));
+  // what sixteen waves hold is one chunk: no records, one launch less
+  if (seqlen <= (force && *force ? c.waves : kMaxWaves) * run) {
+    c.chunks = 1;
+    c.waves = static_cast<int>(div_up64(seqlen, run));
+  }
   return c;
 }
 
@@ -656,26 +652,16 @@ static int64_t record_bytes(const Cut& c) {
   return c.chunks <= 1 ? 0 : 16 + c.chains * c.chunks * c.v * 64 * 8;
 }
 
-// The query does not see the tensors' alignment: the larger of the two layouts.
-static int64_t work_bytes(int dtype, int64_t batch, int64_t seqlen, int64_t dim, int run,
-                          bool parts) {
-  int64_t most = 0;
-  for (int pairs = 0; pairs <= (dtype != 0); ++pairs) {
-    const Cut c = cut_of(pairs != 0, batch, seqlen, dim, run);
-    const int64_t bytes = record_bytes(c) + (parts ? batch * c.chunks * dim * 4 : 0);
-    most = bytes > most ? bytes : most;
-  }
-  return most;
-}
 int64_t gated_fwd_work(int dtype, int64_t batch, int64_t seqlen, int64_t dim) {
-  return work_bytes(dtype, batch, seqlen, dim, kGatedRun, false);
+  return record_bytes(cut_of(dtype, batch, seqlen, dim, kGatedRun));
 }
 int64_t gated_bwd_work(int dtype, int64_t batch, int64_t seqlen, int64_t dim) {
-  return work_bytes(dtype, batch, seqlen, dim, kBwdRun, true);
+  const Cut c = cut_of(dtype, batch, seqlen, dim, kBwdRun);
+  return record_bytes(c) + batch * c.chunks * dim * 4;
 }
 
 static GatedGrid grid_of(const GatedArgs& a, int run, int* v, hipStream_t stream) {
-  const Cut c = cut_of(pairs_of_channels(a), a.batch, a.seqlen, a.dim, run);
+  const Cut c = cut_of(a.dtype, a.batch, a.seqlen, a.dim, run);
   GatedGrid g = {};
   g.n_cblk = static_cast<int>(div_up64(a.dim, 64 * c.v));
   g.chains = static_cast<int>(c.chains);
@@ -727,9 +713,11 @@ hipError_t launch_gated_fwd(const GatedArgs& a, hipStream_t stream) {
 
 hipError_t launch_gated_bwd(const GatedArgs& a, hipStream_t stream) {
   int v;
-  const GatedGrid g = grid_of(a, kBwdRun, &v, stream);
+  GatedGrid g = grid_of(a, kBwdRun, &v, stream);
+  if (a.batch * g.chunks == 1) g.part = a.dlog_decay;  // one row: the sum itself
   SSM_LAUNCH_GATED(gated_bwd_kernel);
-  launch_column_sum(g.part, a.batch * g.chunks, a.dim, a.dlog_decay, stream);
+  if (a.batch * g.chunks > 1)
+    launch_column_sum(g.part, a.batch * g.chunks, a.dim, a.dlog_decay, stream);
   return hipGetLastError();
 }
 

@@ -6,6 +6,54 @@
 
 namespace ssm {
 
+// Vector accesses at the element's alignment: gfx950 runs in unaligned access
+// mode, so a row that starts anywhere moves in whole vectors all the same.
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+typedef u32x4 u32x4_any __attribute__((aligned(2)));
+typedef uint32_t u32_any __attribute__((aligned(2)));
+
+// 8 consecutive values as stored.
+template <typename T>
+struct Run8 : Run<T, 8> {
+  using Run<T, 8>::w;
+  __device__ __forceinline__ void load(const T* p) {
+    const u32x4_any* q = reinterpret_cast<const u32x4_any*>(p);
+#pragma unroll
+    for (int i = 0; i < Run<T, 8>::NW / 4; ++i) {
+      const u32x4 v = q[i];
+      w[4 * i] = v[0]; w[4 * i + 1] = v[1]; w[4 * i + 2] = v[2]; w[4 * i + 3] = v[3];
+    }
+  }
+};
+
+// Stores values 0 .. last (of 8) at p; all of them as vectors, past the caches
+// with STREAM.
+template <typename T, bool STREAM = false>
+__device__ __forceinline__ void store8(T* p, const float (&v)[8], int last = 7) {
+  if (last < 7) {
+#pragma unroll
+    for (int k = 0; k < 7; ++k)
+      if (k <= last) store_act(p, k, v[k]);
+    return;
+  }
+  u32x4_any* q = reinterpret_cast<u32x4_any*>(p);
+  auto put = [&](int i, u32x4 t) {
+    if constexpr (STREAM)
+      __builtin_nontemporal_store(t, q + i);
+    else
+      q[i] = t;
+  };
+  if constexpr (sizeof(T) == 2) {
+    put(0, u32x4{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
+                 pack_bf16x2(v[6], v[7])});
+  } else {
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+      put(i, u32x4{__float_as_uint(v[4 * i]), __float_as_uint(v[4 * i + 1]),
+                   __float_as_uint(v[4 * i + 2]), __float_as_uint(v[4 * i + 3])});
+  }
+}
+
 // v's exchange with the lane `ROR` places further in its row of 16.
 template <int ROR>
 __device__ __forceinline__ float row_ror(float v) {

@@ -79,6 +79,9 @@ def _row_stride(t, name, dtype, shape, device):
     if t.is_contiguous():
         return dim
     strides = t.stride()
+    if len(shape) == 3 and shape[1] > 1 and strides[2] == 1 and strides[1] >= dim \
+            and strides[0] == strides[1] * shape[1]:
+        return strides[1]
     if dim > 1 and strides[-1] != 1:
         raise ValueError(f"{name} must be contiguous in its last dimension")
     ld, rows = None, 1
