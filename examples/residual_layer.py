@@ -1,0 +1,187 @@
+"""A stack of residual layers around the gated linear recurrence: packed
+prefill and token-by-token decode with 8-bit projections, and a training step.
+
+One layer is
+
+    s      = residual + y                    rms_norm_fp8: one pass gives s and
+    q      = norm(s), in 8 bits              the next product's input
+    x,r,i  = columns of q W_in^T + b         fp8_linear
+    h      = recurrence(x, r, i)             gated_scan_fwd / gated_state_update
+    y      = (h in 8 bits) W_out^T           fp8_quantize, fp8_linear
+
+Training keeps the projections in bfloat16 (PyTorch's product) between
+rms_norm_fwd/bwd and gated_scan_fwd/bwd.
+
+    python examples/residual_layer.py [--layers 4 --dim 768 --inner 1536 ...]
+"""
+import argparse
+import os
+import sys
+import time
+
+import torch
+
+sys.path.insert(0, os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
+
+import selective_state_space_38_amd as ssm  # noqa: E402
+
+
+class Layer:
+    """Parameters of one layer, drawn from a seed (random, not trained)."""
+
+    def __init__(self, dim, inner, seed, device="cuda"):
+        gen = torch.Generator().manual_seed(seed)
+
+        def normal(rows, cols):
+            return (torch.randn(rows, cols, generator=gen) * cols ** -0.5).to(device)
+
+        self.dim, self.inner = dim, inner
+        self.norm = torch.ones(dim, device=device)
+        self.w_in = normal(3 * inner, dim)                 # rows: x, r, i
+        self.b_in = torch.zeros(3 * inner, device=device)
+        self.w_out = normal(dim, inner)
+        # per-step decays from 0.9 to 0.999 at r = 0, where sigmoid(r) = 1/2
+        decay = torch.linspace(0.9, 0.999, inner, dtype=torch.float64)
+        self.log_decay = (2 * decay.log()).float().to(device)
+
+    def serve(self):
+        """Lays the weights out for serving: 8 bits, a scale per 128 x 128."""
+        self.w_in8 = ssm.fp8_quantize_weight(self.w_in)
+        self.w_out8 = ssm.fp8_quantize_weight(self.w_out)
+        return self
+
+    def _project(self, y, residual):
+        q, scale, residual = ssm.rms_norm_fp8(y, self.norm, residual=residual,
+                                              residual_out=residual)
+        p = ssm.fp8_linear(q, scale, *self.w_in8, bias=self.b_in)
+        return p.split(self.inner, dim=-1), residual       # column slices, no copies
+
+    def prefill(self, y, residual, reset=None):
+        """y, residual [batch, L, dim] -> y, residual, state [batch, inner]."""
+        (x, r, i), residual = self._project(y, residual)
+        h, state = ssm.gated_scan_fwd(x, r, i, self.log_decay, reset=reset,
+                                      return_last_state=True)
+        return ssm.fp8_linear(*ssm.fp8_quantize(h), *self.w_out8), residual, state
+
+    def step(self, y, residual, state):
+        """y, residual [batch, dim] -> y, residual; state is updated."""
+        (x, r, i), residual = self._project(y, residual)
+        h = ssm.gated_state_update(state, x, r, i, self.log_decay)
+        return ssm.fp8_linear(*ssm.fp8_quantize(h), *self.w_out8), residual
+
+
+def prefill(layers, tokens, reset=None):
+    """tokens [batch, L, dim] bfloat16 -> float32 outputs, the layers' states."""
+    y, residual, states = tokens, torch.zeros_like(tokens, dtype=torch.float32), []
+    for layer in layers:
+        y, residual, state = layer.prefill(y, residual, reset)
+        states.append(state)
+    return residual + y, states
+
+
+def decode(layers, token, states):
+    """token [batch, dim] bfloat16 -> float32 output; states are updated."""
+    y, residual = token, torch.zeros_like(token, dtype=torch.float32)
+    for layer, state in zip(layers, states):
+        y, residual = layer.step(y, residual, state)
+    return residual + y
+
+
+class Norm(torch.autograd.Function):
+    """(y, residual) -> (norm(s), s), s = residual + y."""
+
+    @staticmethod
+    def forward(ctx, y, residual, weight):
+        out, s = ssm.rms_norm_fwd(y, weight, residual=residual)
+        ctx.save_for_backward(s, weight)
+        return out, s
+
+    @staticmethod
+    def backward(ctx, dout, dres):
+        s, weight = ctx.saved_tensors
+        g = ssm.rms_norm_bwd(dout.contiguous(), s, weight, dres=dres.contiguous())
+        return g["ds"].to(dout.dtype), g["ds"], g["dweight"]
+
+
+class Recurrence(torch.autograd.Function):
+    """x, r, i -> h; keeps the state of every 16th step for the backward."""
+
+    @staticmethod
+    def forward(ctx, x, r, i, log_decay, reset):
+        ckpt = ssm.gated_ckpt_buffer(x)
+        out = ssm.gated_scan_fwd(x, r, i, log_decay, reset=reset, ckpt=ckpt)
+        ctx.save_for_backward(x, r, i, log_decay, reset, ckpt)
+        return out
+
+    @staticmethod
+    def backward(ctx, dout):
+        x, r, i, log_decay, reset, ckpt = ctx.saved_tensors
+        g = ssm.gated_scan_bwd(x, r, i, log_decay, dout.contiguous(), reset=reset, ckpt=ckpt)
+        return g["dx"], g["dr"], g["di"], g["dlog_decay"], None
+
+
+def train(layers, tokens, target, reset, steps, rate=1e-2):
+    """Plain gradient descent on a squared error; returns the losses."""
+    names = ("norm", "w_in", "b_in", "w_out", "log_decay")
+    params = [getattr(layer, n).requires_grad_() for layer in layers for n in names]
+    losses = []
+    for _ in range(steps):
+        y, residual = tokens, torch.zeros_like(tokens, dtype=torch.float32)
+        for layer in layers:
+            u, residual = Norm.apply(y, residual, layer.norm)
+            p = u.flatten(0, 1) @ layer.w_in.bfloat16().t() + layer.b_in.bfloat16()
+            x, r, i = p.view(*u.shape[:2], -1).split(layer.inner, dim=-1)
+            h = Recurrence.apply(x, r, i, layer.log_decay, reset)
+            y = (h.flatten(0, 1) @ layer.w_out.bfloat16().t()).view_as(tokens)
+        loss = (residual + y - target).square().mean()
+        grads = torch.autograd.grad(loss, params)
+        with torch.no_grad():
+            for p, g in zip(params, grads):
+                p -= rate * g * p.numel() ** 0.5 / (g.norm() + 1e-12) * p.abs().mean()
+            for layer in layers:
+                layer.log_decay.clamp_(max=-1e-6)           # decays stay below 1
+        losses.append(loss.detach())
+    for p in params:
+        p.requires_grad_(False)
+    return [float(v) for v in losses]
+
+
+def main():
+    ap = argparse.ArgumentParser(description=__doc__.split("\n\n")[0])
+    ap.add_argument("--layers", type=int, default=4)
+    ap.add_argument("--dim", type=int, default=768)
+    ap.add_argument("--inner", type=int, default=1536)
+    ap.add_argument("--batch", type=int, default=4)
+    ap.add_argument("--seqlen", type=int, default=2048)
+    ap.add_argument("--steps", type=int, default=64, help="decoded tokens")
+    ap.add_argument("--train-steps", type=int, default=10)
+    args = ap.parse_args()
+    gen = torch.Generator().manual_seed(0)
+    layers = [Layer(args.dim, args.inner, k) for k in range(args.layers)]
+    tokens = torch.randn(args.batch, args.seqlen, args.dim, generator=gen).bfloat16().cuda()
+    reset = torch.rand(args.batch, args.seqlen, generator=gen).cuda() < 4 / args.seqlen
+
+    target = tokens.float().cumsum(1) * 0.1
+    losses = train(layers, tokens, target, reset, args.train_steps)
+    print(f"training: loss {losses[0]:.4f} -> {losses[-1]:.4f} in {args.train_steps} steps")
+
+    for layer in layers:
+        layer.serve()
+    for timed in (False, True):
+        torch.cuda.synchronize()
+        start = time.perf_counter()
+        _, states = prefill(layers, tokens, reset)
+        torch.cuda.synchronize()
+        middle = time.perf_counter()
+        for t in range(args.steps):
+            decode(layers, tokens[:, t].contiguous(), states)
+        torch.cuda.synchronize()
+        end = time.perf_counter()
+    print(f"prefill: {args.batch} x {args.seqlen} tokens in {(middle - start) * 1e3:.2f} ms")
+    print(f"decode: {(end - middle) / max(args.steps, 1) * 1e6:.0f} us a step of "
+          f"{args.batch} sequences")
+    ssm.check_device_errors()
+
+
+if __name__ == "__main__":
+    main()
