@@ -138,7 +138,7 @@ __device__ __forceinline__ void look_back(const uint64_t* rec, int newest, int s
 
 // R rows of V channels per lane as loaded; rows past the last (n of them)
 // repeat it.  base and ld are the wave's, off is the lane's byte offset.
-template <typename T, int V, int R>
+template <typename T, int V, int R, bool STREAM>
 struct Rows {
   uint32_t w[R];
   __device__ __forceinline__ void load(const void* base, int64_t elem0, int64_t ld, uint32_t off,
@@ -148,8 +148,10 @@ struct Rows {
     for (int j = 0; j < R; ++j) {
       const T* p = add_bytes(row, off);
       row += j + 1 < n ? ld : 0;
-      if constexpr (sizeof(T) * V == 4)
+      if constexpr (STREAM)
         w[j] = __builtin_nontemporal_load(reinterpret_cast<const u32_any*>(p));
+      else if constexpr (sizeof(T) * V == 4)
+        w[j] = *reinterpret_cast<const u32_any*>(p);
       else
         w[j] = *p;
     }
@@ -165,16 +167,23 @@ struct Rows {
   }
 };
 
-template <typename T, int V>
+template <typename T, int V, bool STREAM>
 __device__ __forceinline__ void store_row(void* base, int64_t elem, uint32_t off,
                                           const float (&v)[V]) {
   T* p = add_bytes(static_cast<T*>(base) + elem, off);
-  if constexpr (V == 2)
-    __builtin_nontemporal_store(pack_bf16x2(v[0], v[1]), reinterpret_cast<u32_any*>(p));
-  else if constexpr (sizeof(T) == 4)
-    __builtin_nontemporal_store(v[0], p);
-  else
+  if constexpr (sizeof(T) * V == 4) {
+    uint32_t t;
+    if constexpr (V == 2)
+      t = pack_bf16x2(v[0], v[1]);
+    else
+      t = __float_as_uint(v[0]);
+    if constexpr (STREAM)
+      __builtin_nontemporal_store(t, reinterpret_cast<u32_any*>(p));
+    else
+      *reinterpret_cast<u32_any*>(p) = t;
+  } else {
     store_act(p, 0, v[0]);
+  }
 }
 
 // Where a wave works: one run of one channel block.
@@ -190,6 +199,7 @@ struct GatedGrid {
   int* ticket;
   uint64_t* rec;
   float* part;       // backward: dlog_decay of every (batch row, chunk), [..][dim]
+  bool stream;       // the arrays' rows are whole cache lines, each read or written once
 };
 
 template <int R, bool MULTI, bool REVERSE>
@@ -284,7 +294,7 @@ __device__ __forceinline__ void exchange(const GatedGrid& g, const Place& q, int
   for (int v = 0; v < V; ++v) sh.carry[lane * V + v] = h[v];
 }
 
-template <typename T, int V, bool RESET, bool MULTI>
+template <typename T, int V, bool STREAM, bool RESET, bool MULTI>
 __global__ __launch_bounds__(64 * kMaxWaves) void gated_fwd_kernel(GatedArgs p, GatedGrid g) {
   constexpr int R = kGatedRun;
   __shared__ Shared<V> sh;
@@ -312,7 +322,7 @@ __global__ __launch_bounds__(64 * kMaxWaves) void gated_fwd_kernel(GatedArgs p, 
   uint32_t cut = 0;
   if (n > 0) {
     const int64_t row = q.b * L + q.t0;
-    Rows<T, V, R> x, r, in;
+    Rows<T, V, R, STREAM> x, r, in;
     r.load(p.r, row * p.ld_r + cb, p.ld_r, off, n);
     in.load(p.i, row * p.ld_i + cb, p.ld_i, off, n);
     x.load(p.x, row * p.ld_x + cb, p.ld_x, off, n);
@@ -388,7 +398,7 @@ __global__ __launch_bounds__(64 * kMaxWaves) void gated_fwd_kernel(GatedArgs p, 
     const bool since = RESET && (cut & ((2u << j) - 1)) != 0;
 #pragma unroll
     for (int v = 0; v < V; ++v) o[v] = since ? H[j][v] : fmaf(A[j][v], h[v], H[j][v]);
-    if (p.out && j < n) store_row<T, V>(p.out, (row + j) * D + cb, off, o);
+    if (p.out && j < n) store_row<T, V, STREAM>(p.out, (row + j) * D + cb, off, o);
   }
   if (p.last_state && q.t0 + n == L) {
 #pragma unroll
@@ -405,7 +415,7 @@ __global__ __launch_bounds__(64 * kMaxWaves) void gated_fwd_kernel(GatedArgs p, 
 // the chunks as h does forward (chunks are taken from the sequence's end).
 constexpr int kBwdRun = kGatedRun / 2;
 
-template <typename T, int V, bool RESET, bool MULTI>
+template <typename T, int V, bool STREAM, bool RESET, bool MULTI>
 __global__ __launch_bounds__(64 * kMaxWaves) void gated_bwd_kernel(GatedArgs p, GatedGrid g) {
   constexpr int R = kBwdRun;
   __shared__ Shared<V> sh;
@@ -428,7 +438,7 @@ __global__ __launch_bounds__(64 * kMaxWaves) void gated_bwd_kernel(GatedArgs p, 
     lam[v] = p.log_decay[c + v];
     last[v] = p.dlast ? p.dlast[q.b * D + c + v] : 0.0f;
   }
-  Rows<T, V, R> x, r, in, dout;
+  Rows<T, V, R, STREAM> x, r, in, dout;
   float a[R][V], beta[R][V], before[R][V], start[V];
   float A[V], H[V];
 #pragma unroll
@@ -534,9 +544,9 @@ __global__ __launch_bounds__(64 * kMaxWaves) void gated_bwd_kernel(GatedArgs p, 
         dlam[v] += dl;
       }
       if (live) {
-        store_row<T, V>(p.dx, (row + j) * D + cb, off, dx);
-        store_row<T, V>(p.dr, (row + j) * D + cb, off, dr);
-        store_row<T, V>(p.di, (row + j) * D + cb, off, di);
+        store_row<T, V, STREAM>(p.dx, (row + j) * D + cb, off, dx);
+        store_row<T, V, STREAM>(p.dr, (row + j) * D + cb, off, dr);
+        store_row<T, V, STREAM>(p.di, (row + j) * D + cb, off, di);
       }
     }
     if (p.dh0 && q.t0 == 0 && live) {
@@ -619,18 +629,21 @@ struct Cut {
   int v, waves;
   int64_t chains, chunks;
 };
-// Two bfloat16 channels per lane where there is work for every CU all the same.  Eight waves a workgroup; sixteen where a sequence has many chunks and
-// few channel blocks, since what bounds it then is the hop from chunk to chunk
-// (70 ns each; a million steps of 64 bfloat16 channels: 261 us so, 448 with two
-// channels per lane, 478 with eight waves, 856 with both; of 256 float32
-// channels 764 us against 912), while more blocks run faster with two
+// Two bfloat16 channels per lane where that fills them and there is work for
+// every CU all the same (batch 8, 16000 steps: 128 channels 46 us against 48, 1536
+// 335 against 427, but 64 channels 44 against 30; batch 3, 4000 steps, 320
+// channels 23.5 against 21.1).  Eight waves a workgroup; sixteen where a sequence
+// has many chunks and few channel blocks, since what bounds it then is the hop
+// from chunk to chunk (70 ns each; a million steps of 64 bfloat16 channels: 261 us
+// so, 448 with two channels per lane, 478 with eight waves, 856 with both; of 256
+// float32 channels 764 us against 912), while more blocks run faster with two
 // workgroups on a CU (2.8B-shaped layer 284 us against 334, four waves 304).
 // SSM_FORCE_GATED_WAVES overrides (tests, tuning).
 static Cut cut_of(int dtype, int64_t batch, int64_t seqlen, int64_t dim, int run) {
   Cut c;
   const int64_t chunks = div_up64(seqlen, 8 * run);
-  const bool pairs = dtype != 0 && batch * div_up64(dim, 64) > 2;
-  c.v = pairs && dim > 1 && batch * div_up64(dim, 128) * chunks >= 256 ? 2 : 1;
+  const bool pairs = dtype != 0 && dim > 64 && batch * div_up64(dim, 64) > 2;
+  c.v = pairs && batch * div_up64(dim, 128) * chunks >= 768 ? 2 : 1;
   c.chains = batch * div_up64(dim, 64 * c.v);
   c.waves = c.chains <= 8 && c.chains * chunks >= 512 ? 16 : 8;
   const char* force = getenv("SSM_FORCE_GATED_WAVES");
@@ -660,6 +673,20 @@ int64_t gated_bwd_work(int dtype, int64_t batch, int64_t seqlen, int64_t dim) {
   return record_bytes(c) + batch * c.chunks * dim * 4;
 }
 
+// Rows that are whole cache lines stream past the caches (16384 steps of 5120
+// bfloat16 channels 155 us against 161, backward 299 against 312); parts of lines
+// meet in them (9000 steps of 1001 float32 channels, batch 4: 144 us against 166,
+// backward 278 against 335).
+static bool whole_lines(const GatedArgs& a) {
+  const int64_t size = a.dtype == 0 ? 4 : 2;
+  uint64_t bits = (a.dim | a.ld_x | a.ld_r | a.ld_i) * size;
+  for (const void* t : {a.x, a.r, a.i, a.dout, static_cast<const void*>(a.out),
+                        static_cast<const void*>(a.dx), static_cast<const void*>(a.dr),
+                        static_cast<const void*>(a.di)})
+    bits |= reinterpret_cast<uintptr_t>(t);
+  return bits % 128 == 0;
+}
+
 static GatedGrid grid_of(const GatedArgs& a, int run, int* v, hipStream_t stream) {
   const Cut c = cut_of(a.dtype, a.batch, a.seqlen, a.dim, run);
   GatedGrid g = {};
@@ -667,6 +694,7 @@ static GatedGrid grid_of(const GatedArgs& a, int run, int* v, hipStream_t stream
   g.chains = static_cast<int>(c.chains);
   g.chunks = static_cast<int>(c.chunks);
   g.waves = c.waves;
+  g.stream = whole_lines(a);
   *v = c.v;
   const int64_t bytes = record_bytes(c);
   if (bytes) {
@@ -683,25 +711,29 @@ static GatedGrid grid_of(const GatedArgs& a, int run, int* v, hipStream_t stream
   do {                                                                                      \
     const dim3 grid(static_cast<unsigned>(g.chains) * static_cast<unsigned>(g.chunks));     \
     const dim3 block(64 * g.waves);                                                         \
-    if (a.dtype == 0) {                                                                     \
-      SSM_LAUNCH_GATED_T(KERNEL, float, 1);                                                 \
+    if (a.dtype == 0 && g.stream) {                                                         \
+      SSM_LAUNCH_GATED_T(KERNEL, float, 1, true);                                           \
+    } else if (a.dtype == 0) {                                                              \
+      SSM_LAUNCH_GATED_T(KERNEL, float, 1, false);                                          \
+    } else if (v == 2 && g.stream) {                                                        \
+      SSM_LAUNCH_GATED_T(KERNEL, bf16_t, 2, true);                                          \
     } else if (v == 2) {                                                                    \
-      SSM_LAUNCH_GATED_T(KERNEL, bf16_t, 2);                                                \
+      SSM_LAUNCH_GATED_T(KERNEL, bf16_t, 2, false);                                         \
     } else {                                                                                \
-      SSM_LAUNCH_GATED_T(KERNEL, bf16_t, 1);                                                \
+      SSM_LAUNCH_GATED_T(KERNEL, bf16_t, 1, false);                                         \
     }                                                                                       \
   } while (0)
-#define SSM_LAUNCH_GATED_T(KERNEL, T, V)                                                    \
+#define SSM_LAUNCH_GATED_T(KERNEL, T, V, NT)                                                \
   if (g.chunks > 1) {                                                                       \
     if (a.reset)                                                                            \
-      KERNEL<T, V, true, true><<<grid, block, 0, stream>>>(a, g);                           \
+      KERNEL<T, V, NT, true, true><<<grid, block, 0, stream>>>(a, g);                       \
     else                                                                                    \
-      KERNEL<T, V, false, true><<<grid, block, 0, stream>>>(a, g);                          \
+      KERNEL<T, V, NT, false, true><<<grid, block, 0, stream>>>(a, g);                      \
   } else {                                                                                  \
     if (a.reset)                                                                            \
-      KERNEL<T, V, true, false><<<grid, block, 0, stream>>>(a, g);                          \
+      KERNEL<T, V, NT, true, false><<<grid, block, 0, stream>>>(a, g);                      \
     else                                                                                    \
-      KERNEL<T, V, false, false><<<grid, block, 0, stream>>>(a, g);                         \
+      KERNEL<T, V, NT, false, false><<<grid, block, 0, stream>>>(a, g);                     \
   }
 
 hipError_t launch_gated_fwd(const GatedArgs& a, hipStream_t stream) {
