@@ -283,7 +283,7 @@ int fp8_quantize(const void* x, void* q, float* scale, const norm_dims* dims, vo
 int64_t rms_norm_bwd_work_bytes(const norm_dims* dims) {
   const int rc = check_norm(dims);
   if (rc != SSM_OK) return rc;
-  return up16(ssm::norm_bwd_work(dims->dtype, dims->residual_dtype, dims->rows, dims->dim));
+  return up16(ssm::norm_bwd_work(dims->rows, dims->dim));
 }
 
 int rms_norm_bwd(const void* dy, const void* s, const float* weight, float eps,

@@ -26,9 +26,8 @@ struct Run8 : Run<T, 8> {
   }
 };
 
-// Stores values 0 .. last (of 8) at p; all of them as vectors, past the caches
-// with STREAM.
-template <typename T, bool STREAM = false>
+// Stores values 0 .. last (of 8) at p; all of them as vectors.
+template <typename T>
 __device__ __forceinline__ void store8(T* p, const float (&v)[8], int last = 7) {
   if (last < 7) {
 #pragma unroll
@@ -37,20 +36,14 @@ __device__ __forceinline__ void store8(T* p, const float (&v)[8], int last = 7) 
     return;
   }
   u32x4_any* q = reinterpret_cast<u32x4_any*>(p);
-  auto put = [&](int i, u32x4 t) {
-    if constexpr (STREAM)
-      __builtin_nontemporal_store(t, q + i);
-    else
-      q[i] = t;
-  };
   if constexpr (sizeof(T) == 2) {
-    put(0, u32x4{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
-                 pack_bf16x2(v[6], v[7])});
+    q[0] = u32x4{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
+                 pack_bf16x2(v[6], v[7])};
   } else {
 #pragma unroll
     for (int i = 0; i < 2; ++i)
-      put(i, u32x4{__float_as_uint(v[4 * i]), __float_as_uint(v[4 * i + 1]),
-                   __float_as_uint(v[4 * i + 2]), __float_as_uint(v[4 * i + 3])});
+      q[i] = u32x4{__float_as_uint(v[4 * i]), __float_as_uint(v[4 * i + 1]),
+                   __float_as_uint(v[4 * i + 2]), __float_as_uint(v[4 * i + 3])};
   }
 }
 

@@ -75,7 +75,7 @@ struct NormArgs {
   void* work;
 };
 
-int64_t norm_bwd_work(int dtype, int residual_dtype, int64_t rows, int64_t dim);
+int64_t norm_bwd_work(int64_t rows, int64_t dim);
 hipError_t launch_norm_fwd(const NormArgs& a, hipStream_t stream);
 // norm: y = rms norm of x + residual; otherwise y = x
 hipError_t launch_norm_fp8(const NormArgs& a, bool norm, hipStream_t stream);

@@ -3,10 +3,12 @@
 // backward, for gfx950.
 //
 // All of it streams: a row is read once into registers, reduced there, and
-// written once.  Rows of up to 4096 values belong to one wave (no LDS, no
-// barrier: lane l holds the runs of 8 values l, l + 64, ..., 16 bytes of
-// bfloat16 each), longer ones to the four waves of a workgroup.  A group of 128
-// values is then 16 neighbouring lanes' runs, one DPP row.  A wave walks rows a
+// written once.  A row belongs to LANES threads, which hold its runs of 8 values
+// l, l + LANES, ... (16 bytes of bfloat16 each): 16 lanes up to 256 values, a
+// wave up to some 3000 (neither needs LDS or a barrier), the four waves of a
+// workgroup beyond.  A group of 128 values is 16 neighbouring lanes' runs, one DPP row.
+// Short rows, such as a head's, by 16 lanes: 200000 x 64 float32 values 32 us
+// against 51 a wave each, backward 34 against 72.  A wave walks rows a
 // grid apart with the weights in registers.  32768 rows of 2560 bfloat16 values:
 // with a float32 residual and 8-bit output 176 us, the training pair 258 us,
 // 5.2 TB/s each, the rate of a large copy.
@@ -48,32 +50,37 @@ struct RowRuns {
   }
 };
 
-// Sum over the WPR waves that share a row, in every thread.
-template <int WPR>
+// Sum over the LANES threads that share a row, in every thread.
+template <int LANES>
 __device__ __forceinline__ float row_sum(float v, float* lds) {
+  if constexpr (LANES == 16) return row16_sum(v);
   v = wave_sum(v);
-  if constexpr (WPR == 1) {
-    return v;
-  } else {
+  if constexpr (LANES == 256) {
     if ((threadIdx.x & 63) == 0) lds[threadIdx.x >> 6] = v;
     __syncthreads();
     v = (lds[0] + lds[1]) + (lds[2] + lds[3]);
     __syncthreads();
-    return v;
   }
+  return v;
+}
+template <int LANES>
+__device__ __forceinline__ double row_sum(double v, float*) {
+  static_assert(LANES == 16, "short rows only");
+#pragma unroll
+  for (int d = 8; d; d >>= 1) v += __shfl_xor(v, d, 64);
+  return v;
 }
 
 struct None {};  // no residual
 
 // S: the residual's type, or None.  NORM = false: y = x (8-bit output only).
-template <typename T, typename S, bool FP8, bool NORM, int NV, int WPR, bool TAIL>
+template <typename T, typename S, bool FP8, bool NORM, int NV, int LANES, bool TAIL>
 __global__ __launch_bounds__(256) void norm_rows_kernel(NormArgs p) {
   constexpr bool kRes = !std::is_same<S, None>::value;
   using R = typename std::conditional<kRes, S, T>::type;
   __shared__ float lds[4];
-  constexpr int LANES = 64 * WPR;
   const RowRuns<LANES, TAIL> q(p.dim);
-  const int64_t step = static_cast<int64_t>(gridDim.x) * (4 / WPR);
+  const int64_t step = static_cast<int64_t>(gridDim.x) * (256 / LANES);
   float w[NV][8];
   if constexpr (NORM) {
 #pragma unroll
@@ -84,7 +91,7 @@ __global__ __launch_bounds__(256) void norm_rows_kernel(NormArgs p) {
       for (int e = 0; e < 8; ++e) w[i][e] = t.get(e);
     }
   }
-  for (int64_t row = static_cast<int64_t>(blockIdx.x) * (4 / WPR) + threadIdx.x / LANES;
+  for (int64_t row = static_cast<int64_t>(blockIdx.x) * (256 / LANES) + threadIdx.x / LANES;
        row < p.rows; row += step) {
     const int64_t base = row * p.dim;
     Run8<T> x[NV];
@@ -111,7 +118,7 @@ __global__ __launch_bounds__(256) void norm_rows_kernel(NormArgs p) {
     }
     float rms = 1.0f, rstd = 1.0f;
     if constexpr (NORM) {
-      const float var = row_sum<WPR>(ss, lds) / static_cast<float>(p.dim) + p.eps;
+      const float var = row_sum<LANES>(ss, lds) / static_cast<float>(p.dim) + p.eps;
       rms = sqrtf(var);
       rstd = 1.0f / rms;
     }
@@ -143,17 +150,20 @@ __global__ __launch_bounds__(256) void norm_rows_kernel(NormArgs p) {
   }
 }
 
-// Backward: ds = rstd (w dy - s rstd^2 mean(w dy s)) + dres.  Every wave keeps
-// its rows' sum of dy s rstd in registers; a workgroup's four sums meet in LDS
-// and leave as one row of part [workgroups][dim], which a second kernel adds up.
-template <typename T, typename S, int NV, int WPR, bool TAIL>
+// Backward: ds = rstd (w dy - s rstd^2 mean(w dy s)) + dres.  Every thread keeps
+// its rows' sum of dy s rstd in registers; a workgroup's sums meet in LDS and
+// leave as one row of part [workgroups][dim], which a second kernel adds up.
+//
+// F: the row's sums and ds in double where there are few columns, since the two
+// terms of ds then all but cancel (with one column they leave eps / s^2 of
+// themselves).
+template <typename T, typename S, typename F, int NV, int LANES, bool TAIL>
 __global__ __launch_bounds__(256) void norm_bwd_rows_kernel(NormArgs p, float* part) {
   __shared__ float lds[4];
-  __shared__ float s_dw[WPR == 1 ? 64 * NV * 8 : 1];
-  constexpr int LANES = 64 * WPR;
+  __shared__ float s_dw[LANES <= 64 ? 64 * NV * 8 : 1];
   const RowRuns<LANES, TAIL> q(p.dim);
-  const int64_t step = static_cast<int64_t>(gridDim.x) * (4 / WPR);
-  const float inv_dim = 1.0f / static_cast<float>(p.dim);
+  const int64_t step = static_cast<int64_t>(gridDim.x) * (256 / LANES);
+  const F inv_dim = F(1) / static_cast<F>(p.dim);
   float w[NV][8], dw[NV][8];
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
@@ -165,7 +175,7 @@ __global__ __launch_bounds__(256) void norm_bwd_rows_kernel(NormArgs p, float* p
       dw[i][e] = 0.0f;
     }
   }
-  for (int64_t row = static_cast<int64_t>(blockIdx.x) * (4 / WPR) + threadIdx.x / LANES;
+  for (int64_t row = static_cast<int64_t>(blockIdx.x) * (256 / LANES) + threadIdx.x / LANES;
        row < p.rows; row += step) {
     const int64_t base = row * p.dim;
     Run8<S> s[NV], dres[NV];
@@ -176,129 +186,71 @@ __global__ __launch_bounds__(256) void norm_bwd_rows_kernel(NormArgs p, float* p
       q.load(static_cast<const T*>(p.dy) + base, i, dy[i]);
       if (p.dres) q.load(static_cast<const S*>(p.dres) + base, i, dres[i]);
     }
-    float ss = 0.0f, dot = 0.0f;
+    F ss = 0, dot = 0;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      float a = 0.0f, b = 0.0f;
+      F a = 0, b = 0;
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        const float v = q.get(s[i], i, e);
-        a = fmaf(v, v, a);
-        b = fmaf(dy[i].get(e) * w[i][e], v, b);
+        const F v = q.get(s[i], i, e);
+        a = fma(v, v, a);
+        b = fma(static_cast<F>(dy[i].get(e)) * static_cast<F>(w[i][e]), v, b);
       }
-      ss += q.on(i) ? a : 0.0f;
-      dot += q.on(i) ? b : 0.0f;
+      ss += q.on(i) ? a : F(0);
+      dot += q.on(i) ? b : F(0);
     }
-    ss = row_sum<WPR>(ss, lds);
-    dot = row_sum<WPR>(dot, lds);
-    const float rstd = 1.0f / sqrtf(ss * inv_dim + p.eps);
-    const float k = rstd * rstd * (dot * inv_dim);
+    ss = row_sum<LANES>(ss, lds);
+    dot = row_sum<LANES>(dot, lds);
+    const F rstd = F(1) / sqrt(ss * inv_dim + static_cast<F>(p.eps));
+    const F k = rstd * rstd * (dot * inv_dim);
+    const float rstd32 = static_cast<float>(rstd);
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       float g[8];
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        const float v = s[i].get(e), d = dy[i].get(e);
-        dw[i][e] = fmaf(d, v * rstd, dw[i][e]);
-        g[e] = rstd * fmaf(-v, k, d * w[i][e]);
-        if (p.dres) g[e] += dres[i].get(e);
+        const F v = s[i].get(e), d = dy[i].get(e);
+        dw[i][e] = fmaf(static_cast<float>(d), static_cast<float>(v) * rstd32, dw[i][e]);
+        F t = rstd * fma(-v, k, d * static_cast<F>(w[i][e]));
+        if (p.dres) t += static_cast<F>(dres[i].get(e));
+        g[e] = static_cast<float>(t);
       }
       if (q.on(i)) store8(static_cast<S*>(p.ds) + base + q.at(i), g, q.last_of(i));
     }
   }
-  if constexpr (WPR == 1) {
+  if constexpr (LANES == 16) {  // the wave's four rows at a time
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        dw[i][e] += __shfl_xor(dw[i][e], 16, 64);
+        dw[i][e] += __shfl_xor(dw[i][e], 32, 64);
+      }
+  }
+  if constexpr (LANES <= 64) {
     for (int k = 0; k < 4; ++k) {
       if (threadIdx.x >> 6 == static_cast<unsigned>(k)) {
 #pragma unroll
         for (int i = 0; i < NV; ++i)
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
-            float* t = &s_dw[(e * NV + i) * 64 + q.lane];
+            float* t = &s_dw[(e * NV + i) * 64 + (threadIdx.x & 63)];
             dw[i][e] = k ? *t + dw[i][e] : dw[i][e];
             *t = dw[i][e];
           }
       }
       __syncthreads();
     }
-    if (threadIdx.x < 192) return;  // the last wave holds the sums
+    if (threadIdx.x < 256 - LANES) return;  // the last wave holds the sums
   }
 #pragma unroll
   for (int i = 0; i < NV; ++i)
     if (q.on(i)) store8(part + blockIdx.x * p.dim + q.at(i), dw[i], q.last_of(i));
 }
 
-// ---- backward of few columns: a workgroup per row, element by element ----
-
-__device__ __forceinline__ float load_as(const void* p, int dtype, int64_t i) {
-  return dtype == 0 ? static_cast<const float*>(p)[i] : to_f32(static_cast<const bf16_t*>(p)[i]);
-}
-__device__ __forceinline__ void store_as(void* p, int dtype, int64_t i, float v) {
-  if (dtype == 0)
-    static_cast<float*>(p)[i] = v;
-  else
-    store_act(static_cast<bf16_t*>(p), i, v);
-}
-
-// Sum over a workgroup of four waves, returned in every thread.
-template <typename F>
-__device__ __forceinline__ F block_sum(F v, F* lds) {
-  for (int d = 32; d; d >>= 1) v += __shfl_xor(v, d, 64);
-  if ((threadIdx.x & 63) == 0) lds[threadIdx.x >> 6] = v;
-  __syncthreads();
-  v = (lds[0] + lds[1]) + (lds[2] + lds[3]);
-  __syncthreads();
-  return v;
-}
-
-// In 64 bits: with few columns the two terms of ds all but cancel (with one
-// column they leave eps / s^2 of themselves).
-__global__ __launch_bounds__(256) void norm_bwd_few_kernel(NormArgs p, float* rstds) {
-  __shared__ double lds[4];
-  const int64_t row = blockIdx.x, base = row * p.dim;
-  const int dim = static_cast<int>(p.dim);
-  double ss = 0.0, dot = 0.0;
-  for (int c = threadIdx.x; c < dim; c += 256) {
-    const double v = load_as(p.s, p.residual_dtype, base + c);
-    ss = fma(v, v, ss);
-    dot = fma(static_cast<double>(load_as(p.dy, p.dtype, base + c)) * p.weight[c], v, dot);
-  }
-  ss = block_sum(ss, lds);
-  dot = block_sum(dot, lds);
-  const double var = ss / dim + p.eps;
-  const double rstd = 1.0 / sqrt(var);
-  const double k = dot / (dim * var);
-  for (int c = threadIdx.x; c < dim; c += 256) {
-    const double v = load_as(p.s, p.residual_dtype, base + c);
-    double g = rstd * (static_cast<double>(load_as(p.dy, p.dtype, base + c)) * p.weight[c] - v * k);
-    if (p.dres) g += load_as(p.dres, p.residual_dtype, base + c);
-    store_as(p.ds, p.residual_dtype, base + c, static_cast<float>(g));
-  }
-  if (threadIdx.x == 0) rstds[row] = static_cast<float>(rstd);
-}
-
-// dweight of a slab of rows: part[slab][c], 4 waves taking every 4th row.
-constexpr int kSlab = 256;
-__global__ __launch_bounds__(256) void norm_dweight_few_kernel(NormArgs p, const float* rstds,
-                                                               float* part) {
-  __shared__ float lds[4][64];
-  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
-  const int64_t c = static_cast<int64_t>(blockIdx.x) * 64 + lane;
-  const int64_t r0 = static_cast<int64_t>(blockIdx.y) * kSlab;
-  const int64_t r1 = r0 + kSlab < p.rows ? r0 + kSlab : p.rows;
-  float sum = 0.0f;
-  if (c < p.dim)
-    for (int64_t row = r0 + w; row < r1; row += 4)
-      sum = fmaf(load_as(p.dy, p.dtype, row * p.dim + c),
-                 load_as(p.s, p.residual_dtype, row * p.dim + c) * rstds[row], sum);
-  lds[w][lane] = sum;
-  __syncthreads();
-  if (w == 0 && c < p.dim)
-    part[blockIdx.y * p.dim + c] = (lds[0][lane] + lds[1][lane]) + (lds[2][lane] + lds[3][lane]);
-}
-
 // ---- host ----
 
-// Backward rows shorter than this go through the kernels for few columns.
+// Backward rows shorter than this are summed in double.
 constexpr int64_t kFewColumns = 64;
 
 static unsigned count(int64_t n, int64_t per, int64_t most) {
@@ -306,26 +258,32 @@ static unsigned count(int64_t n, int64_t per, int64_t most) {
   return static_cast<unsigned>(k < most ? k : most);
 }
 
-// One wave per row up to 4096 values, four beyond; NV runs of 8 per lane.
-#define SSM_NORM_BY_SIZE(LAUNCH)                 \
+// NV runs of 8 a thread, LANES threads a row; MOST: the longest rows, in runs, of
+// a wave.  Forward 448: 16384 rows of 2688 values 98 us against 103 by four waves,
+// but 8192 of 4096 81 against 76.  Backward, with twice the registers, 320: 16384
+// of 2688 127 us by a wave against 116, 8192 of 4096 100 against 91.
+#define SSM_NORM_BY_SIZE(LAUNCH, MOST)           \
   do {                                           \
     const int64_t runs = div_up64(a.dim, 8);     \
-    if (runs <= 64) LAUNCH(1, 1);                \
-    else if (runs <= 128) LAUNCH(2, 1);          \
-    else if (runs <= 192) LAUNCH(3, 1);          \
-    else if (runs <= 320) LAUNCH(5, 1);          \
-    else if (runs <= 512) LAUNCH(8, 1);          \
-    else if (runs <= 768) LAUNCH(3, 4);          \
-    else if (runs <= 1024) LAUNCH(4, 4);         \
-    else LAUNCH(8, 4);                           \
+    if (runs <= 16) LAUNCH(1, 16);               \
+    else if (runs <= 32) LAUNCH(2, 16);          \
+    else if (runs <= 64) LAUNCH(1, 64);          \
+    else if (runs <= 128) LAUNCH(2, 64);         \
+    else if (runs <= 192) LAUNCH(3, 64);         \
+    else if (runs <= 320) LAUNCH(5, 64);         \
+    else if (runs <= MOST) LAUNCH(MOST / 64, 64); \
+    else if (runs <= 512) LAUNCH(2, 256);        \
+    else if (runs <= 768) LAUNCH(3, 256);        \
+    else if (runs <= 1024) LAUNCH(4, 256);       \
+    else LAUNCH(8, 256);                         \
   } while (0)
 
 template <typename T, typename S, bool FP8, bool NORM, bool TAIL>
 static void launch_rows_cut(const NormArgs& a, hipStream_t stream) {
-#define SSM_LAUNCH(NV, WPR)                                                                 \
-  norm_rows_kernel<T, S, FP8, NORM, NV, WPR, TAIL>                                          \
-      <<<count(a.rows, 4 / WPR, 256 * 8), 256, 0, stream>>>(a)
-  SSM_NORM_BY_SIZE(SSM_LAUNCH);
+#define SSM_LAUNCH(NV, LANES)                                                               \
+  norm_rows_kernel<T, S, FP8, NORM, NV, LANES, TAIL>                                        \
+      <<<count(a.rows, 256 / LANES, 256 * 8), 256, 0, stream>>>(a)
+  SSM_NORM_BY_SIZE(SSM_LAUNCH, 448);
 #undef SSM_LAUNCH
 }
 
@@ -364,19 +322,22 @@ hipError_t launch_norm_fp8(const NormArgs& a, bool norm, hipStream_t stream) {
 
 constexpr int64_t kBwdGroups = 512;  // workgroups of the backward, two per CU
 
-int64_t norm_bwd_work(int, int, int64_t rows, int64_t dim) {
-  const int64_t slabs = div_up64(rows, kSlab), groups = rows < kBwdGroups ? rows : kBwdGroups;
-  const int64_t any = div_up64(rows, 4) * 16 + slabs * dim * 4;
-  return any > groups * dim * 4 ? any : groups * dim * 4;
+int64_t norm_bwd_work(int64_t rows, int64_t dim) {
+  return (rows < kBwdGroups ? rows : kBwdGroups) * dim * 4;
 }
 
 template <typename T, typename S, bool TAIL>
 static unsigned launch_bwd_rows_cut(const NormArgs& a, float* part, hipStream_t stream) {
   unsigned grid = 0;
-#define SSM_LAUNCH(NV, WPR)                                                         \
-  (grid = count(a.rows, 4 / WPR, kBwdGroups),                                       \
-   norm_bwd_rows_kernel<T, S, NV, WPR, TAIL><<<grid, 256, 0, stream>>>(a, part))
-  SSM_NORM_BY_SIZE(SSM_LAUNCH);
+#define SSM_LAUNCH_AS(F, NV, LANES)                                                     \
+  (grid = count(a.rows, 256 / LANES, kBwdGroups),                                       \
+   norm_bwd_rows_kernel<T, S, F, NV, LANES, TAIL><<<grid, 256, 0, stream>>>(a, part))
+#define SSM_LAUNCH(NV, LANES) SSM_LAUNCH_AS(float, NV, LANES)
+  if (a.dim < kFewColumns)
+    SSM_LAUNCH_AS(double, 1, 16);
+  else
+    SSM_NORM_BY_SIZE(SSM_LAUNCH, 320);
+#undef SSM_LAUNCH_AS
 #undef SSM_LAUNCH
   return grid;
 }
@@ -388,23 +349,15 @@ static unsigned launch_bwd_rows(const NormArgs& a, float* part, hipStream_t stre
 }
 
 hipError_t launch_norm_bwd(const NormArgs& a, hipStream_t stream) {
-  float* work = static_cast<float*>(a.work);
-  if (a.dim >= kFewColumns) {
-    unsigned rows;
-    if (a.dtype == 0)
-      rows = a.residual_dtype == 0 ? launch_bwd_rows<float, float>(a, work, stream)
-                                   : launch_bwd_rows<float, bf16_t>(a, work, stream);
-    else
-      rows = a.residual_dtype == 0 ? launch_bwd_rows<bf16_t, float>(a, work, stream)
-                                   : launch_bwd_rows<bf16_t, bf16_t>(a, work, stream);
-    launch_column_sum(work, rows, a.dim, a.dweight, stream);
-  } else {
-    float* part = work + div_up64(a.rows, 4) * 4;
-    const unsigned slabs = count(a.rows, kSlab, a.rows);
-    norm_bwd_few_kernel<<<static_cast<unsigned>(a.rows), 256, 0, stream>>>(a, work);
-    norm_dweight_few_kernel<<<dim3(count(a.dim, 64, a.dim), slabs), 256, 0, stream>>>(a, work, part);
-    launch_column_sum(part, slabs, a.dim, a.dweight, stream);
-  }
+  float* part = static_cast<float*>(a.work);
+  unsigned rows;
+  if (a.dtype == 0)
+    rows = a.residual_dtype == 0 ? launch_bwd_rows<float, float>(a, part, stream)
+                                 : launch_bwd_rows<float, bf16_t>(a, part, stream);
+  else
+    rows = a.residual_dtype == 0 ? launch_bwd_rows<bf16_t, float>(a, part, stream)
+                                 : launch_bwd_rows<bf16_t, bf16_t>(a, part, stream);
+  launch_column_sum(part, rows, a.dim, a.dweight, stream);
   return hipGetLastError();
 }
 
