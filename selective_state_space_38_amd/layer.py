@@ -102,9 +102,9 @@ def _row_stride(t, name, dtype, shape, device):
     return ld
 
 
-def _like(x, shape):
-    """A contiguous tensor of x's type."""
-    return torch.empty_like(x) if x.is_contiguous() else x.new_empty(shape)
+def _like(x):
+    """A contiguous tensor of x's type and shape (torch.empty costs 0.5 us more)."""
+    return torch.empty_like(x, memory_format=torch.contiguous_format)
 
 
 def _work(nbytes, device):
@@ -174,11 +174,12 @@ def gated_scan_fwd(x, r, i, log_decay, reset=None, h0=None, return_last_state=Fa
     _check(h0, "h0", torch.float32, (bsz, dim), dev)
     _check_ckpt(ckpt, dims, dev)
     if out is None:
-        out = _like(x, shape)
+        out = _like(x)
     else:
         _check(out, "out", x.dtype, shape, dev)
     if return_last_state and last_state is None:
-        last_state = torch.empty((bsz, dim), dtype=torch.float32, device=dev)
+        last_state = (torch.empty((bsz, dim), dtype=torch.float32, device=dev) if h0 is None
+                      else torch.empty_like(h0))
     _check(last_state, "last_state", torch.float32, (bsz, dim), dev)
     lib = _lib.load()
     with _on(dev):
@@ -212,10 +213,10 @@ def gated_scan_bwd(x, r, i, log_decay, dout, reset=None, h0=None, dlast=None, ck
     _check(dout, "dout", x.dtype, shape, dev)
     _check(dlast, "dlast", torch.float32, (bsz, dim), dev)
     _check_ckpt(ckpt, dims, dev)
-    g = {k: _like(x, shape) for k in ("dx", "dr", "di")}
-    g["dlog_decay"] = torch.empty(dim, dtype=torch.float32, device=dev)
+    g = {k: _like(x) for k in ("dx", "dr", "di")}
+    g["dlog_decay"] = torch.empty_like(log_decay)
     if h0 is not None:
-        g["dh0"] = torch.empty((bsz, dim), dtype=torch.float32, device=dev)
+        g["dh0"] = torch.empty_like(h0)
     lib = _lib.load()
     with _on(dev):
         work = _work(lib.gated_scan_bwd_work_bytes(byref(dims), int(ckpt is not None)),
@@ -241,7 +242,7 @@ def gated_state_update(state, x, r, i, log_decay, out=None):
         raise ValueError("state is required")
     _check(state, "state", torch.float32, shape, dev)
     if out is None:
-        out = _like(x, shape)
+        out = _like(x)
     else:
         _check(out, "out", x.dtype, shape, dev)
     with _on(dev):
@@ -353,8 +354,7 @@ def rms_norm_bwd(dy, s, weight, eps=1e-5, dres=None):
     _check(weight, "weight", torch.float32, (dim,), dev)
     _check(dres, "dres", s.dtype, shape, dev)
     dims = _lib.NormDims(rows, dim, code, scode)
-    g = dict(ds=torch.empty_like(s),
-             dweight=torch.empty(dim, dtype=torch.float32, device=dev))
+    g = dict(ds=torch.empty_like(s), dweight=torch.empty_like(weight))
     lib = _lib.load()
     with _on(dev):
         work = _work(lib.rms_norm_bwd_work_bytes(byref(dims)), dev)
