@@ -644,6 +644,9 @@ int fp8_linear(const void* xq, const float* x_scale, const void* wq,
                const float* w_scale, const float* bias, void* out, void* work,
                const linear_dims* dims, void* stream);
 
+/* As ssm_check_device_errors, of the gated recurrence's carry waits. */
+int gated_check_device_errors(void* stream);
+
 /* Static, human-readable name of a status code (never NULL). */
 const char* ssm_status_string(int status);
 

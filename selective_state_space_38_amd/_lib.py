@@ -59,6 +59,7 @@ EXPORTED = (
     "fp8_linear",
     "ssm_status_string",
     "ssm_check_device_errors",
+    "gated_check_device_errors",
     "ssm_fwd_plan_for",
 )
 
@@ -254,6 +255,8 @@ def load():
     lib.ssm_status_string.restype = ctypes.c_char_p
     lib.ssm_check_device_errors.argtypes = [vp]
     lib.ssm_check_device_errors.restype = ctypes.c_int
+    lib.gated_check_device_errors.argtypes = [vp]
+    lib.gated_check_device_errors.restype = ctypes.c_int
     lib.ssm_fwd_plan_for.argtypes = [dims_p, ctypes.POINTER(SsmFwdPlan)]
     lib.ssm_fwd_plan_for.restype = ctypes.c_int
     _lib = lib

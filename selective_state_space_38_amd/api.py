@@ -478,4 +478,7 @@ def mamba_block_fwd(x_in, weights, out=None):
 def check_device_errors(device=None):
     """Synchronises the current stream and raises if a carry wait timed out."""
     dev = torch.device("cuda", torch.cuda.current_device()) if device is None else device
-    _raise(_lib.load().ssm_check_device_errors(_stream(dev)))
+    lib, stream = _lib.load(), _stream(dev)
+    status = [lib.ssm_check_device_errors(stream), lib.gated_check_device_errors(stream)]
+    _raise(status[0])
+    _raise(status[1])

@@ -9,7 +9,6 @@
 #include <hip/hip_runtime.h>
 
 #include "../../include/ssm_scan.h"
-#include "layer_internal.h"
 #include "ssm_internal.h"
 
 namespace {
@@ -924,14 +923,13 @@ const char* ssm_status_string(int status) {
 }
 
 int ssm_check_device_errors(void* stream) {
-  unsigned c32 = 0, c16 = 0, cb = 0, cg = 0;
+  unsigned c32 = 0, c16 = 0, cb = 0;
   const hipStream_t st = static_cast<hipStream_t>(stream);
   if (ssm::fwd_f32::read_and_clear_errors(st, &c32) != hipSuccess ||
       ssm::fwd_bf16::read_and_clear_errors(st, &c16) != hipSuccess ||
-      ssm::read_and_clear_bwd_errors(st, &cb) != hipSuccess ||
-      ssm::read_and_clear_gated_errors(st, &cg) != hipSuccess)
+      ssm::read_and_clear_bwd_errors(st, &cb) != hipSuccess)
     return SSM_ELAUNCH;
-  return (c32 || c16 || cb || cg) ? SSM_ETIMEOUT : SSM_OK;
+  return (c32 || c16 || cb) ? SSM_ETIMEOUT : SSM_OK;
 }
 
 int ssm_fwd_plan_for(const ssm_dims* dims, ssm_fwd_plan* plan) {

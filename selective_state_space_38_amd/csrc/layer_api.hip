@@ -259,6 +259,13 @@ int gated_state_update(float* state, const void* x, const void* r, const void* i
                                                                                   : SSM_ELAUNCH;
 }
 
+int gated_check_device_errors(void* stream) {
+  unsigned count = 0;
+  if (ssm::read_and_clear_gated_errors(static_cast<hipStream_t>(stream), &count) != hipSuccess)
+    return SSM_ELAUNCH;
+  return count ? SSM_ETIMEOUT : SSM_OK;
+}
+
 int rms_norm_fwd(const void* x, const void* residual, const float* weight, float eps, void* y,
                  void* residual_out, const norm_dims* dims, void* stream) {
   if (!y) return SSM_EINVAL;
