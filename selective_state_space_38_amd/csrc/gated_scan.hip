@@ -635,23 +635,39 @@ struct Cut {
   int v, waves;
   int64_t chains, chunks;
 };
-// Two bfloat16 channels per lane where that fills them and there is work for
-// every CU all the same (batch 8, 16000 steps: 128 channels 46 us against 48, 1536
-// 335 against 427, but 64 channels 44 against 30; batch 3, 4000 steps, 320
-// channels 23.5 against 21.1).  Eight waves a workgroup; sixteen where a sequence
-// has many chunks and few channel blocks, since what bounds it then is the hop
-// from chunk to chunk (70 ns each; a million steps of 64 bfloat16 channels: 261 us
-// so, 448 with two channels per lane, 478 with eight waves, 856 with both; of 256
-// float32 channels 764 us against 912), while more blocks run faster with two
-// workgroups on a CU (2.8B-shaped layer 284 us against 334, four waves 304).
+// A pass whose workgroups are at most one a CU takes the fewest waves, eight to
+// sixteen, for which that holds (2 x 535 steps of 5056 bfloat16 channels: 18.7 us
+// so, 21.7 with eight), first with one channel per lane, then, of bfloat16, with
+// two where more than 64 channels fill them (64 channels, batch 8, 16000 steps: 44
+// us against 30).  Larger ones have two workgroups of eight waves on a CU
+// (2.8B-shaped layer 284 us against 334 with sixteen, 304 with four), backward
+// sixteen waves up to some 1500 workgroups (2 x 2048 x 2560: 47.5 us against 50.3,
+// but 2 x 4096 x 5120 147 against 143).  Where a long sequence has few channel
+// blocks, what bounds it is the hop from chunk to chunk (70 ns each), so the
+// chunks are large (a million steps of 64 bfloat16 channels: 261 us, 448 with two
+// channels per lane, 478 with eight waves, 856 with both; of 256 float32 channels
+// 764 us against 912).
 // SSM_FORCE_GATED_WAVES overrides (tests, tuning).
 static Cut cut_of(int dtype, int64_t batch, int64_t seqlen, int64_t dim, int run) {
+  const int64_t runs = div_up64(seqlen, run);
+  auto one_a_cu = [&](int64_t chains) {
+    for (int w = 8; w <= kMaxWaves; w += 2)
+      if (chains * div_up64(runs, w) <= 256) return w;
+    return 0;
+  };
   Cut c;
-  const int64_t chunks = div_up64(seqlen, 8 * run);
-  const bool pairs = dtype != 0 && dim > 64 && batch * div_up64(dim, 64) > 2;
-  c.v = pairs && batch * div_up64(dim, 128) * chunks >= 768 ? 2 : 1;
-  c.chains = batch * div_up64(dim, 64 * c.v);
-  c.waves = c.chains <= 8 && c.chains * chunks >= 512 ? 16 : 8;
+  c.v = 1;
+  c.chains = batch * div_up64(dim, 64);
+  c.waves = one_a_cu(c.chains);
+  if (!c.waves && dtype != 0 && dim > 64 && c.chains > 8) {
+    c.v = 2;
+    c.chains = batch * div_up64(dim, 128);
+    c.waves = one_a_cu(c.chains);
+  }
+  if (!c.waves) {
+    const bool few = run == kBwdRun && c.chains * div_up64(runs, kMaxWaves) <= 1500;
+    c.waves = c.chains <= 8 || few ? kMaxWaves : 8;
+  }
   const char* force = getenv("SSM_FORCE_GATED_WAVES");
   if (force && *force) {
     const int w = atoi(force) & ~1;  // the backward's waves work in pairs
