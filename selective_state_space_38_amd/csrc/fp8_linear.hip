@@ -142,10 +142,15 @@ __global__ __launch_bounds__(1024) void fp8_stream_kernel(LinearArgs p) {
 // (t / 2) 32 + (i / 4) 8 + (t % 2) 4 + i % 4 of the wave's: two tiles give a lane
 // 8 consecutive outputs to store.
 //
-// The one barrier of a block stands before its last row of tiles, when every
-// operand of the block has been read from LDS: behind it the buffer takes the
-// block after next, and the next block's first operands are read while the last
-// row is multiplied.
+// The barrier of a block stands before its last row of tiles, when every operand
+// of the block has been read from LDS: behind it the buffer takes the block after
+// next, and the next block's first operands are read while the last row is
+// multiplied.
+//
+// Tiles of 128 outputs by 256 tokens (ONE) keep a single buffer for the tokens,
+// whose block is in registers once its first row of tiles is multiplied: a second
+// barrier there, and it takes the next block.  So two workgroups fit a CU, each
+// multiplying while the other waits, starts or stores.
 
 typedef const __attribute__((address_space(1))) void* global_ptr;
 typedef __attribute__((address_space(3))) void* lds_ptr;
@@ -224,14 +229,14 @@ __device__ __forceinline__ void tile_of(int64_t tiles_m, int64_t tiles_n, int64_
 }
 
 template <typename T, int BN, int BM, int WN, int WM>
-__global__ __launch_bounds__(64 * WN * WM) void fp8_tile_kernel(LinearArgs p) {
+__global__ __launch_bounds__(64 * WN * WM, 2) void fp8_tile_kernel(LinearArgs p) {
   constexpr int WAVES = WN * WM, NT = BN / WN / 16, MT = BM / WM / 16;
-  constexpr bool EXACT = sizeof(T) == 4;
+  constexpr bool EXACT = sizeof(T) == 4, ONE = BM > BN;
   // separate objects, so that reads of one are known not to wait for loads into another
   __shared__ __align__(1024) uint8_t s_w0[BN * kFp8Group];
   __shared__ __align__(1024) uint8_t s_w1[BN * kFp8Group];
   __shared__ __align__(1024) uint8_t s_x0[BM * kFp8Group];
-  __shared__ __align__(1024) uint8_t s_x1[BM * kFp8Group];
+  __shared__ __align__(1024) uint8_t s_x1[ONE ? 16 : BM * kFp8Group];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wn = wave % WN, wm = wave / WN;
@@ -280,7 +285,7 @@ __global__ __launch_bounds__(64 * WN * WM) void fp8_tile_kernel(LinearArgs p) {
   __syncthreads();
   if (groups > 1) {
     lw.load(gw + kFp8Group, s_w1, wave, lane, k - kFp8Group);
-    lx.load(gx + kFp8Group, s_x1, wave, lane, k - kFp8Group);
+    if constexpr (!ONE) lx.load(gx + kFp8Group, s_x1, wave, lane, k - kFp8Group);
   }
 
   const int i = lane & 15, quad = lane >> 4;
@@ -321,6 +326,12 @@ __global__ __launch_bounds__(64 * WN * WM) void fp8_tile_kernel(LinearArgs p) {
     for (int t = 0; t < NT * MT; ++t) {
       const int n = t / MT, m = t % MT;
       if (m == 0) {
+        if (ONE && n == 1 && g + 1 < groups) {
+          // every wave's tokens are in registers: LDS reads only are waited for
+          lds_barrier();
+          const int at = (g + 1) * kFp8Group;
+          lx.load(gx + at, cx, wave, lane, k - at);
+        }
         if (n + 1 < NT) {
           a[(n + 1) & 1] = read_w(cw, n + 1);
         } else {
@@ -347,15 +358,16 @@ __global__ __launch_bounds__(64 * WN * WM) void fp8_tile_kernel(LinearArgs p) {
     if (g + 2 < groups) {
       const int at = (g + 2) * kFp8Group;
       lw.load(gw + at, cw, wave, lane, k - at);
-      lx.load(gx + at, cx, wave, lane, k - at);
+      if constexpr (!ONE) lx.load(gx + at, cx, wave, lane, k - at);
     }
   };
+  uint8_t* const x1 = ONE ? s_x0 : s_x1;
   int g = 0;
   for (; g + 1 < groups; g += 2) {
-    step(g, s_w0, s_x0, s_w1, s_x1);
-    step(g + 1, s_w1, s_x1, s_w0, s_x0);
+    step(g, s_w0, s_x0, s_w1, x1);
+    step(g + 1, s_w1, x1, s_w0, s_x0);
   }
-  if (g < groups) step(g, s_w0, s_x0, s_w1, s_x1);
+  if (g < groups) step(g, s_w0, s_x0, s_w1, x1);
 
   // Of bfloat16 outputs the wave's tile goes through LDS, where the operands were,
   // so that whole rows of it leave at a time: a lane's own 8 outputs of a token
@@ -381,9 +393,11 @@ __global__ __launch_bounds__(64 * WN * WM) void fp8_tile_kernel(LinearArgs p) {
     if constexpr (sizeof(O) == 2) {
       constexpr int kBytes = N * M * 2;
       constexpr int kPer = BN * kFp8Group / kBytes;  // waves' tiles in an operand's buffer
-      static_assert(BN == BM && kPer * 4 >= WAVES, "the buffers are of one size");
+      static_assert(ONE ? BM == 2 * BN && kPer * 4 == WAVES : BN == BM && kPer * 4 >= WAVES,
+                    "room for every wave's tile");
       const int at = wave / kPer;
-      uint8_t* lds = (at == 0 ? s_w0 : at == 1 ? s_w1 : at == 2 ? s_x0 : s_x1) + wave % kPer * kBytes;
+      uint8_t* lds = at == 0 ? s_w0 : at == 1 ? s_w1 : at == 2 ? s_x0 : ONE ? s_x0 + kPer * kBytes : s_x1;
+      lds += wave % kPer * kBytes;
       auto key = [](int tok) { return tok / (16 / C) & (C - 1); };
       __syncthreads();  // no wave reads operands any more
 #pragma unroll
@@ -407,7 +421,7 @@ __global__ __launch_bounds__(64 * WN * WM) void fp8_tile_kernel(LinearArgs p) {
         O* to = out + row * p.n + n;
         if (n + 8 <= p.n) {
           // the largest tiles' outputs exceed the caches: they stream past them
-          if constexpr (BN * BM == 65536)
+          if constexpr (BM == 256)
             __builtin_nontemporal_store(v, reinterpret_cast<u32x4_any*>(to));
           else
             *reinterpret_cast<u32x4_any*>(to) = v;
@@ -491,7 +505,7 @@ __global__ __launch_bounds__(256) void quantize_weight_kernel(const T* w, int64_
   if (threadIdx.x == 0) scale[blockIdx.x] = m / kFp8Max;
 }
 
-enum Shape : int { kStream = 0, kTile64 = 1, kTile128 = 2, kTile256 = 3 };
+enum Shape : int { kStream = 0, kTile64 = 1, kTile128 = 2, kTile256 = 3, kTile128x256 = 4 };
 constexpr int64_t kStreamRows = 32;  // most tokens of the streaming kernel
 
 struct Plan {
@@ -505,11 +519,14 @@ static int forced(const char* name) {
 
 // Few tokens stream the weights.  More take the largest tile of which there are
 // enough: with fewer tiles than CUs, the smaller tile's larger share of loads
-// costs less than the idle CUs (measured over 320 to 5120 outputs and 768 to
-// 5120 inputs: 160 tiles of 256 x 256 38 us where 640 of 128 x 128 take 46, but
-// 80 take 62 against 47; 320 of 128 x 128 27 us against 33 for 64 x 64, 160 37
-// against 33; float32 outputs, two workgroups of 128 x 128 on a CU matching 256 x
-// 256, 640 65 against 79, 320 77 against 74).
+// costs less than the idle CUs (bfloat16 outputs: 160 tiles of 256 x 256 36 us
+// where 640 of 128 x 128 take 42, but 80 take 60 against 40; 320 of 128 x 128 23.5
+// us against 31 for 64 x 64, 160 36 against 30; float32 outputs: 480 of 128 x 128
+// 43 us against 53, 320 44 against 41).  Tiles of 256 x 256 come one a CU at a
+// time, so where their last round leaves more than a tenth of the CUs idle, tiles
+// of 128 x 256, two a CU, are taken: 4096 x 5120 x 2560 (1.25 rounds) 61 us against
+// 72, 8192 x 2560 x 5120 (1.25) 112 against 128, 8192 x 5120 x 2560 (2.5) 97
+// against 108; but 32768 x 5120 x 2560 (10) 408 against 384.
 //
 // 64 x 64 tiles may split the inputs into parts.  Measured: about 0.42 us a
 // block; for the join 2 us, its traffic, written and read at 2.5 TB/s, and its
@@ -523,7 +540,8 @@ static Plan plan_of(int dtype, int64_t rows, int64_t n, int64_t k) {
   auto tiles = [&](int64_t side) { return div_up64(n, side) * div_up64(rows, side); };
   if (rows > kStreamRows) {
     if (dtype != 0 && tiles(256) >= 150) {
-      q.shape = kTile256;
+      const int64_t t = tiles(256), rounds = div_up64(t, 256);
+      q.shape = rounds > 1 && 10 * t < 9 * 256 * rounds ? kTile128x256 : kTile256;
     } else if (tiles(128) >= (dtype == 0 ? 384 : 256)) {
       q.shape = kTile128;
     } else {
@@ -539,8 +557,8 @@ static Plan plan_of(int dtype, int64_t rows, int64_t n, int64_t k) {
       }
     }
   }
-  if (shape >= 0 && shape <= kTile256 && (shape != kStream || rows <= kStreamRows) &&
-      (shape != kTile256 || dtype != 0)) {
+  if (shape >= 0 && shape <= kTile128x256 && (shape != kStream || rows <= kStreamRows) &&
+      (shape < kTile256 || dtype != 0)) {
     q.shape = shape;
     q.parts = 1;
   }
@@ -584,9 +602,12 @@ static void launch_linear_typed(const LinearArgs& a, hipStream_t stream) {
       break;
     case kTile64: launch_tiles<T, 64, 64, 2, 2>(a, q.parts, stream); break;
     case kTile128: launch_tiles<T, 128, 128, 2, 2>(a, q.parts, stream); break;
-    default:
-      // bfloat16 outputs only (float32 ones' widened operands do not fit the registers)
+    // bfloat16 outputs only (float32 ones' widened operands do not fit the registers)
+    case kTile256:
       if constexpr (sizeof(T) == 2) launch_tiles<T, 256, 256, 2, 4>(a, q.parts, stream);
+      break;
+    default:
+      if constexpr (sizeof(T) == 2) launch_tiles<T, 128, 256, 1, 4>(a, q.parts, stream);
   }
 }
 
