@@ -1,5 +1,6 @@
 """A stack of residual layers around the gated linear recurrence: packed
-prefill and token-by-token decode with 8-bit projections, and a training step.
+prefill and token-by-token decode with 8-bit projections (each step from the
+host, then from a captured graph), and a training step.
 
 One layer is
 
@@ -87,6 +88,20 @@ def decode(layers, token, states):
     return residual + y
 
 
+def capture(layers, token, states):
+    """A decode step as a graph, which leaves token and states as they are:
+    (graph, output); a replay decodes what token then holds."""
+    kept = [state.clone() for state in states]
+    decode(layers, token, states)            # allocations and clocks outside the capture
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = decode(layers, token, states)
+    for state, before in zip(states, kept):
+        state.copy_(before)
+    return graph, out
+
+
 class Norm(torch.autograd.Function):
     """(y, residual) -> (norm(s), s), s = residual + y."""
 
@@ -167,7 +182,7 @@ def main():
 
     for layer in layers:
         layer.serve()
-    for timed in (False, True):
+    for _ in range(2):  # the first pass warms up
         torch.cuda.synchronize()
         start = time.perf_counter()
         _, states = prefill(layers, tokens, reset)
@@ -180,6 +195,16 @@ def main():
     print(f"prefill: {args.batch} x {args.seqlen} tokens in {(middle - start) * 1e3:.2f} ms")
     print(f"decode: {(end - middle) / max(args.steps, 1) * 1e6:.0f} us a step of "
           f"{args.batch} sequences")
+    token = tokens[:, 0].clone()
+    graph, _ = capture(layers, token, states)
+    torch.cuda.synchronize()
+    start = time.perf_counter()
+    for t in range(args.steps):
+        token.copy_(tokens[:, t])
+        graph.replay()
+    torch.cuda.synchronize()
+    print(f"decode from a graph: {(time.perf_counter() - start) / max(args.steps, 1) * 1e6:.0f} "
+          "us a step")
     ssm.check_device_errors()
 
 

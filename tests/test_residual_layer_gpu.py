@@ -61,6 +61,27 @@ def test_packed_documents_are_apart():
         assert off(got, want) <= 2 ** -4
 
 
+def test_decode_from_a_graph():
+    from residual_layer import capture, decode, prefill
+    layers = stack(256, 384)
+    g = torch.Generator().manual_seed(6)
+    tokens = torch.randn(3, 30, 256, generator=g).bfloat16().cuda()
+    _, states = prefill(layers, tokens[:, :20].contiguous())
+    eager = [s.clone() for s in states]
+    token = tokens[:, 20].contiguous()
+    graph, out = capture(layers, token, states)
+    for got, want in zip(states, eager):
+        assert torch.equal(got, want)
+    for t in range(20, 30):
+        want = decode(layers, tokens[:, t].contiguous(), eager)
+        token.copy_(tokens[:, t])
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, want)
+        for a, b in zip(states, eager):
+            assert torch.equal(a, b)
+
+
 def test_training_lowers_the_loss():
     from residual_layer import Layer, train
     layers = [Layer(128, 192, k) for k in range(2)]
