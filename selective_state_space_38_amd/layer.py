@@ -23,11 +23,12 @@ FP8_GROUP = 128
 # only where it is not the current one (entering it and torch's stream object
 # cost 1.3 and 1.9 us, these two 0.4 together).
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 _NO_CONTEXT = contextlib.nullcontext()
 
 
 def _on(device):
-    if device.index == torch.cuda.current_device():
+    if device.index == _current_device():
         return _NO_CONTEXT
     return torch.cuda.device(device)
 
