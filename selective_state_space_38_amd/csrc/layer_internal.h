@@ -16,11 +16,6 @@ constexpr int kFp8Group = 128;
 constexpr float kFp8Max = 448.0f;                                // largest e4m3 value
 constexpr float kFp8AmaxFloor = 7.888609052210118e-31f;          // 2^-100
 
-// 448 y / m, y's value on the scale of a group whose largest magnitude is m.
-// 448 = 1024 * 7 / 16: the product with 7 / 16 cannot overflow and is exact for
-// a bfloat16 y, so a quotient on a tie between two 8-bit values is exact too.
-__device__ __forceinline__ float fp8_ratio(float y, float m) { return y * 0.4375f / m * 1024.0f; }
-
 struct GatedArgs {
   int dtype;
   int64_t batch, seqlen, dim, ld_x, ld_r, ld_i;
