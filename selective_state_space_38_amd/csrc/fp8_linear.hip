@@ -152,10 +152,10 @@ __global__ __launch_bounds__(1024) void fp8_stream_kernel(LinearArgs p) {
 // barrier there, and it takes the next block.  So two workgroups fit a CU, each
 // multiplying while the other waits, starts or stores.
 //
-// 32768 x 5120 x 2560: bfloat16 outputs 394 to 407 us, 2.1 PFLOP/s, where a library
+// 32768 x 5120 x 2560: bfloat16 outputs 394 to 429 us, 2.1 PFLOP/s, where a library
 // product without block scales takes 301; the matrix pipes are busy half the time
 // (343 us without loads in the loop, 353 without stores, 22 fewer without the
-// scales' FMAs).  float32 outputs, at half the matrix rate, 797.
+// scales' FMAs).  float32 outputs, at half the matrix rate, 797 to 847.
 
 typedef const __attribute__((address_space(1))) void* global_ptr;
 typedef __attribute__((address_space(3))) void* lds_ptr;
