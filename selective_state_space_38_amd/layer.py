@@ -385,12 +385,18 @@ def fp8_quantize_weight(w):
 
 
 def fp8_linear(xq, x_scale, wq, w_scale, bias=None, out_dtype=torch.bfloat16, out=None):
-    """Linear layer on 8-bit operands on the GPU, summed in float32.
+    """Linear layer on 8-bit operands on the GPU.
 
     xq [..., k] float8_e4m3fn with x_scale [ceil(k / 128), rows] (from
     rms_norm_fp8 or fp8_quantize); wq [n, k], w_scale (from
     fp8_quantize_weight); bias: [n] float32.  k must be a multiple of 16.
     Returns out [..., n] in out_dtype (float32 or bfloat16).
+
+    float32 outputs, and bfloat16 ones of up to 32 rows, are summed in float32.
+    bfloat16 outputs of more rows are summed by the 8-bit matrix instruction,
+    128 inputs at a time, which cuts the products of every 8 inputs at 2^-13 of
+    the largest: below the output's own rounding unless the terms cancel.  Where
+    that matters, ask for float32 (half the rate) and convert.
     """
     if not isinstance(xq, torch.Tensor) or not isinstance(wq, torch.Tensor):
         raise TypeError("xq and wq must be torch.Tensors")
