@@ -80,21 +80,22 @@ __device__ __forceinline__ float wave_sum(float v) {
   return (read_lane(v, 0) + read_lane(v, 16)) + (read_lane(v, 32) + read_lane(v, 48));
 }
 
-// Values of a group on the 8-bit scale: 448 y / m by a reciprocal and one
+// Values of a group on the 8-bit scale: 448 (y unit) / m by a reciprocal and one
 // correction.  m's mantissa and exponent are taken apart, so nothing
 // overflows and the reciprocal is of a number in [1/2, 1); 448 = 2^10 7/16 and
-// the product with 7/16 is exact for a bfloat16 y.  The correction leaves the
+// the product with 7/16 is exact for a bfloat16 y where unit is 1.  The correction leaves the
 // quotient within half a unit, so one on a tie between two 8-bit values stays
 // there.
 struct Fp8Scaler {
-  float mant, rcp;
+  float mul, mant, rcp;
   int exp;
-  __device__ __forceinline__ explicit Fp8Scaler(float m)
-      : mant(__builtin_amdgcn_frexp_mantf(m)),
+  __device__ __forceinline__ explicit Fp8Scaler(float m, float unit = 1.0f)
+      : mul(0.4375f * unit),
+        mant(__builtin_amdgcn_frexp_mantf(m)),
         rcp(rcp_hw(mant)),
         exp(10 - __builtin_amdgcn_frexp_expf(m)) {}
   __device__ __forceinline__ float operator()(float y) const {
-    const float a = y * 0.4375f;
+    const float a = y * mul;
     const float t = a * rcp;
     return __builtin_amdgcn_ldexpf(fmaf(fmaf(-t, mant, a), rcp, t), exp);
   }

@@ -116,12 +116,9 @@ __global__ __launch_bounds__(256) void norm_rows_kernel(NormArgs p) {
       if constexpr (kRes)
         if (q.on(i)) store8(static_cast<R*>(p.residual_out) + base + q.at(i), s[i], q.last_of(i));
     }
-    float rms = 1.0f, rstd = 1.0f;
-    if constexpr (NORM) {
-      const float var = row_sum<LANES>(ss, lds) / static_cast<float>(p.dim) + p.eps;
-      rms = sqrtf(var);
-      rstd = 1.0f / rms;
-    }
+    float rstd = 1.0f;
+    if constexpr (NORM)
+      rstd = 1.0f / sqrtf(row_sum<LANES>(ss, lds) / static_cast<float>(p.dim) + p.eps);
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       float y[8];
@@ -132,19 +129,24 @@ __global__ __launch_bounds__(256) void norm_rows_kernel(NormArgs p) {
         for (int e = 0; e < 8; ++e) y[e] *= rstd;
         if (q.on(i)) store8(static_cast<T*>(p.y) + base + q.at(i), y, q.last_of(i));
       } else {
-        // q = 448 y / max |y| does not need rstd; the scale does
+        // q = 448 y / max |y| needs rstd only where the floor decides, or may (the
+        // row holds next to nothing, or an infinity, which makes rstd 0): times a
+        // small or large rms instead, the floor would underflow or overflow
         float m = 0.0f;
 #pragma unroll
         for (int e = 0; e < 8; ++e) m = fmaxf(m, fabsf(y[e]));
-        m = fmaxf(row16_max(q.on(i) ? m : 0.0f), kFp8AmaxFloor * rms);
-        const Fp8Scaler to(m);
+        m = row16_max(q.on(i) ? m : 0.0f);
+        const float top = NORM ? m * rstd : m;
+        const float most = fmaxf(top, kFp8AmaxFloor);
+        const bool plain = m > kFp8AmaxFloor && top >= kFp8AmaxFloor;
+        const Fp8Scaler to(NORM && plain ? m : most, NORM && !plain ? rstd : 1.0f);
 #pragma unroll
         for (int e = 0; e < 8; ++e) y[e] = to(y[e]);
         const int r = i * LANES + q.lane;
         if (q.on(i))
           *reinterpret_cast<uint2*>(p.q + base + r * 8) =
               make_uint2(pack_fp8x4(y[0], y[1], y[2], y[3]), pack_fp8x4(y[4], y[5], y[6], y[7]));
-        if (q.on(i) && (q.lane & 15) == 0) p.scale[(r >> 4) * p.rows + row] = m * rstd / kFp8Max;
+        if (q.on(i) && (q.lane & 15) == 0) p.scale[(r >> 4) * p.rows + row] = most / kFp8Max;
       }
     }
   }
