@@ -83,17 +83,20 @@ __device__ __forceinline__ float wave_sum(float v) {
 // Values of a group on the 8-bit scale: 448 (y unit) / m by a reciprocal and one
 // correction.  m's mantissa and exponent are taken apart, so nothing
 // overflows and the reciprocal is of a number in [1/2, 1); 448 = 2^10 7/16 and
-// the product with 7/16 is exact for a bfloat16 y where unit is 1.  The correction leaves the
-// quotient within half a unit, so one on a tie between two 8-bit values stays
-// there.
+// the product with 7/16 is exact for a bfloat16 y where unit is 1.  The
+// correction leaves the quotient within half a unit, so one on a tie between two
+// 8-bit values stays there.  An infinite m takes finite values to 0.
 struct Fp8Scaler {
   float mul, mant, rcp;
   int exp;
-  __device__ __forceinline__ explicit Fp8Scaler(float m, float unit = 1.0f)
-      : mul(0.4375f * unit),
-        mant(__builtin_amdgcn_frexp_mantf(m)),
-        rcp(rcp_hw(mant)),
-        exp(10 - __builtin_amdgcn_frexp_expf(m)) {}
+  __device__ __forceinline__ explicit Fp8Scaler(float m, float unit = 1.0f) {
+    const bool inf = m == __builtin_inff();
+    mul = inf ? 0.0f : 0.4375f * unit;
+    m = inf ? 1.0f : m;
+    mant = __builtin_amdgcn_frexp_mantf(m);
+    rcp = rcp_hw(mant);
+    exp = 10 - __builtin_amdgcn_frexp_expf(m);
+  }
   __device__ __forceinline__ float operator()(float y) const {
     const float a = y * mul;
     const float t = a * rcp;
