@@ -18,7 +18,8 @@ __device__ unsigned g_gated_timeouts;
 // a = 1 - m, elsewhere from a = exp(y), losing at most ~4e-7 relative.  lam2 =
 // log_decay log2(e), so y2 = y log2(e) is the hardware exp's argument, and the
 // cubic is in y2.  (The kernels' vector units are busy three quarters of the time:
-// the series to y^6 that holds to |y| < 1/4 costs 3% of the forward's time.)
+// the series to y^6 that holds to |y| < 1/4 costs 3% of the forward's time.)  The
+// clamp is for log_decay > 0; unlike fmaxf it keeps a beta that is not a number.
 __device__ __forceinline__ void gate(float r, float lam2, float& rho, float& a, float& beta) {
   rho = sigmoid_f32(r);
   const float y2 = lam2 * rho;
@@ -30,7 +31,7 @@ __device__ __forceinline__ void gate(float r, float lam2, float& rho, float& a, 
   const bool series = fabsf(y2) < 0.27050532f;
   const float m = series ? p * y2 : 1.0f - e;
   a = series ? 1.0f - m : e;
-  beta = __builtin_amdgcn_sqrtf(fmaxf(fmaf(m, a, m), 0.0f));
+  beta = __builtin_amdgcn_sqrtf(__builtin_elementwise_maximum(fmaf(m, a, m), 0.0f));
 }
 
 // A wave owns V channels per lane (one dword of a row: 64 float32 or 128
