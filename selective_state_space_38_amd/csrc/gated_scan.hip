@@ -460,13 +460,14 @@ __global__ __launch_bounds__(64 * CAP, 4) void gated_bwd_kernel(GatedArgs p, Gat
       start[v] = p.ckpt[(q.b * div_up64(L, kGatedRun) + q.t0 / kGatedRun) * D + c + v];
 #pragma unroll
     for (int j = 0; j < R; ++j) {
+      const bool at_reset = RESET && (cut >> j & 1);
       Gates gates;
 #pragma unroll
       for (int v = 0; v < V; ++v) {
         float rho;
         gate(r.get(j, v), lam[v] * kLog2e, rho, a[j][v], beta[j][v]);
         const float io = sigmoid_f32(in.get(j, v));
-        gates[v] = rho;
+        gates[v] = at_reset ? 0.0f : rho;  // r is not used there, whatever it holds
         gates[V + v] = io;
         before[j][v] = io * x.get(j, v);
       }

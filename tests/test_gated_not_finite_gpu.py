@@ -78,3 +78,17 @@ def test_step(dtype):
     out = gated_state_update(state, one["x"], one["r"], one["i"], s["log_decay"])
     check(out[:, None], want[:, None], slice(0, 1), "out")
     check(state[:, None], want_state[:, None], slice(0, 1), "state")
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("bsz,length,dim,at", [(2, 40, 66, 0), (2, 40, 66, 39), (2, 600, 66, 128),
+                                               (2, 2500, 70, 1000), (260, 3, 130, 1)])
+def test_decay_gate_at_a_reset(bsz, length, dim, at, dtype):
+    # a document's first step does not use its decay gate: nothing changes
+    s = make(bsz, length, dim, dtype, resets=[0, at], seed=at)
+    bad = spoilt(s, "r", at)
+    for got, want in zip(forward(bad), forward(s)):
+        assert torch.equal(got, want)
+    got, want = backward(bad), backward(s)
+    for k in want:
+        assert torch.equal(got[k], want[k]), k
