@@ -152,7 +152,9 @@ def train(layers, tokens, target, reset, steps, rate=1e-2):
         grads = torch.autograd.grad(loss, params)
         with torch.no_grad():
             for p, g in zip(params, grads):
-                p -= rate * g * p.numel() ** 0.5 / (g.norm() + 1e-12) * p.abs().mean()
+                # steps in proportion to the parameter; a bias starts from zero
+                size = p.abs().mean().clamp_min(1e-2)
+                p -= rate * g * p.numel() ** 0.5 / (g.norm() + 1e-12) * size
             for layer in layers:
                 layer.log_decay.clamp_(max=-1e-6)           # decays stay below 1
         losses.append(loss.detach())
