@@ -486,6 +486,9 @@ int64_t ssm_ckpt_bytes(const ssm_dims* dims);
  *     points allocate nothing and can be captured into a graph.
  *   - Activations need only their element's alignment unless said otherwise.
  *   - Values that are not finite propagate; a reset drops them (below).
+ *   - The SSM_FORCE_ variables of the environment (tests, tuning) change the
+ *     scratch a call needs: they must not change between a _bytes query and the
+ *     calls that use its answer.
  * ------------------------------------------------------------------------- */
 
 /* Sizes of a gated recurrence.  x, r and i are rows of dim channels (unit
@@ -510,8 +513,8 @@ typedef struct {
  *   x, r, i   : [batch][seqlen][dim] of dtype, row strides above
  *   log_decay : [dim] float32, <= 0 (beta is taken as 0 where 1 - a^2 < 0)
  *   reset     : [batch][seqlen] bytes (nullable): where nonzero a document
- *               starts, a_t = 0 and beta_t = 1, and h_{t-1} is dropped even if
- *               it is not finite
+ *               starts, a_t = 0 and beta_t = 1; neither h_{t-1} nor r_t counts
+ *               there, finite or not
  *   h0        : [batch][dim] float32 (nullable = zeros)
  *   out       : [batch][seqlen][dim] of dtype (nullable if ckpt is given)
  *   last_state: [batch][dim] float32 (nullable), h after the last step
@@ -581,6 +584,7 @@ typedef struct {
  * (OCP e4m3) with a float32 scale for every 128 values of a row:
  *   m = max(max |y| in the group, 2^-100),  q = e4m3(448 y / m),
  *   scale = m / 448,  y ~ q * scale
+ * (the maximum passes over NaNs, whose codes are NaN)
  *   q            : [rows][dim] bytes
  *   scale        : [ceil(dim / 128)][rows] float32
  * and needs dim a multiple of 16 and x, residual, weight, residual_out and q
@@ -615,6 +619,7 @@ int rms_norm_bwd(const void* dy, const void* s, const float* weight, float eps,
  * Weight [n][k] (a linear layer's layout, dtype) in 8 bits with a float32 scale
  * for every tile of 128 x 128 (the last ones smaller), by the rule of
  * rms_norm_fp8 over the tile: q [n][k], scale [ceil(n / 128)][ceil(k / 128)].
+ * Any k is converted, but fp8_linear takes multiples of 16 only.
  */
 int fp8_quantize_weight(const void* w, int dtype, int64_t n, int64_t k,
                         void* q, float* scale, void* stream);

@@ -63,7 +63,7 @@ __device__ __forceinline__ f32x4 mfma_fp8(i32x8 a, i32x8 b) {
 // read 4 x 32 bytes of each row's block, whole cache lines); the activations come
 // from the L2.  The waves' sums meet in LDS and are added in wave order.  Products
 // are summed in float32 for either output type, which costs nothing here.  8
-// tokens, 5120 x 2560 weights: 6.9 us, launch included, 3 us of it a call of any
+// tokens, 5120 x 2560 weights: 6.6 us, launch included, 3 us of it a call of any
 // size; 32 rows a workgroup measured 6.0 there, but 9.0 against 6.7 at 2560 x 5120,
 // where they leave most CUs idle, and more blocks in flight a wave nothing.
 
@@ -160,10 +160,10 @@ __global__ __launch_bounds__(1024) void fp8_stream_kernel(LinearArgs p) {
 // barrier there, and it takes the next block.  So two workgroups fit a CU, each
 // multiplying while the other waits, starts or stores.
 //
-// 32768 x 5120 x 2560: bfloat16 outputs 394 to 429 us, 2.1 PFLOP/s, where a library
+// 32768 x 5120 x 2560: bfloat16 outputs 384 to 429 us by box, 2.1 PFLOP/s, where a library
 // product without block scales takes 301; the matrix pipes are busy half the time
 // (343 us without loads in the loop, 353 without stores, 22 fewer without the
-// scales' FMAs).  float32 outputs, at half the matrix rate, 797 to 847.
+// scales' FMAs).  float32 outputs, at half the matrix rate, 786 to 847.
 
 typedef const __attribute__((address_space(1))) void* global_ptr;
 typedef __attribute__((address_space(3))) void* lds_ptr;
@@ -573,7 +573,7 @@ static int forced(const char* name) {
 // time, so where their last round leaves more than a tenth of the CUs idle, tiles
 // of 128 x 256, two a CU, are taken: 4096 x 5120 x 2560 (1.25 rounds) 61 us against
 // 72, 8192 x 2560 x 5120 (1.25) 112 against 128, 8192 x 5120 x 2560 (2.5) 97
-// against 108; but 32768 x 5120 x 2560 (10) 408 against 384.
+// against 108; but 32768 x 5120 x 2560 (10) 388 against 384.
 //
 // 64 x 64 tiles may split the inputs into parts.  Measured: about 0.42 us a
 // block; for the join 2 us, its traffic, written and read at 2.5 TB/s, and its

@@ -42,7 +42,8 @@ __device__ __forceinline__ void gate(float r, float lam2, float& rho, float& a, 
 // zero; the runs' last ones meet in LDS, and once the state h before the run is
 // known the outputs are A_j h + H_j.  Every input is read once and every output
 // written once: 4 x 8192 steps of 5120 bfloat16 channels 273 us, 4.9 TB/s where a
-// large copy reaches 5.2, the vector units 75% busy; with its backward 770 us, 4.8.
+// large copy reaches 5.2 and three reads to a write 6.0, the vector units 75%
+// busy; with its backward 770 us, 4.8.
 //
 // Chunks of one channel block exchange carries through 8-byte records, one per
 // channel, holding both numbers of an aggregate or the state itself, so a
@@ -609,8 +610,9 @@ __global__ __launch_bounds__(256) void gated_clear_kernel(uint4* p, int64_t n) {
   if (i < n) p[i] = make_uint4(0, 0, 0, 0);
 }
 
-// One step, a thread per channel: 256 x 5120 bfloat16 5.6 us, launch included (21
-// MB, 4 us of a copy's rate).
+// One step, a thread per channel: 256 x 5120 bfloat16 6.1 us, launch included (21
+// MB, 4.1 us of a copy's rate); 8.5 where no cache holds its inputs, float32 10.8
+// (31 MB, 6.1 us).
 template <typename T>
 __global__ __launch_bounds__(256) void gated_step_kernel(GatedArgs p) {
   const int64_t g = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
@@ -645,7 +647,7 @@ struct Cut {
 // so, 21.7 with eight), first with one channel per lane, then, of bfloat16, with
 // two where more than 64 channels fill them (64 channels, batch 8, 16000 steps: 44
 // us against 30).  Larger ones have two workgroups of eight waves on a CU
-// (2.8B-shaped layer 284 us against 334 with sixteen, 304 with four), backward
+// (2.8B-shaped layer 270 us against 324 with sixteen, 301 with four), backward
 // sixteen waves up to some 1500 workgroups (2 x 2048 x 2560: 47.5 us against 50.3,
 // but 2 x 4096 x 5120 147 against 143).  Where a long sequence has few channel
 // blocks, what bounds it is the hop from chunk to chunk (70 ns each), so the

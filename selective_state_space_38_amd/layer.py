@@ -162,7 +162,8 @@ def gated_scan_fwd(x, r, i, log_decay, reset=None, h0=None, return_last_state=Fa
     x, r, i: [batch, L, dim] (float32 or bfloat16, all the same; contiguous,
     or column slices of one projection's output); log_decay: [dim] float32,
     <= 0; reset: [batch, L] bool or uint8, true where a document starts (the
-    state before is dropped and the input taken with weight sigmoid(i));
+    state before is dropped, r is not used and the input is taken with weight
+    sigmoid(i));
     h0: [batch, dim] float32.  ckpt: a buffer from gated_ckpt_buffer() that
     keeps what gated_scan_bwd starts from.
     """
@@ -368,7 +369,8 @@ def rms_norm_bwd(dy, s, weight, eps=1e-5, dres=None):
 def fp8_quantize_weight(w):
     """A linear layer's weight [n, k] (float32 or bfloat16) in 8 bits:
     (wq [n, k] float8_e4m3fn, w_scale [ceil(n / 128), ceil(k / 128)] float32),
-    one scale for every tile of 128 x 128."""
+    one scale for every tile of 128 x 128.  Any k is converted; fp8_linear takes
+    multiples of 16 (pad the inputs with zeros)."""
     code = _act(w, "w")
     if w.dim() != 2:
         raise ValueError("w must be [n, k]")
