@@ -18,8 +18,9 @@ typedef float f32x4 __attribute__((ext_vector_type(4)));
 //
 // The 8-bit matrix instruction does not sum in float32: of 8 consecutive inputs
 // it cuts every product, towards zero, to a multiple of 2^(E - 13), where E is the
-// largest sum of a pair's exponents among the 8 (measured with one product beside
-// a larger one; sums of 8 are then added in float32).  So up to seven products
+// largest sum of a pair's exponents among the 8, a subnormal's counting as -6
+// (measured with one product beside a larger one; sums of 8 are then added in
+// float32).  So up to seven products
 // beside a large one lose less than 2^-13 of it each, at worst 7 2^-13 = 2^-10.2
 // of the largest product of every 8.  A sum of 2560 normal values is off by 1.5e-5
 // of its magnitude; with one input in 128 a thousand times the others the product
