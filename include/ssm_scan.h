@@ -652,6 +652,184 @@ int fp8_linear(const void* xq, const float* x_scale, const void* wq,
                const float* w_scale, const float* bias, void* out, void* work,
                const linear_dims* dims, void* stream);
 
+/* ---------------------------------------------------------------------------
+ * Operators of a feed-forward layer, dense or of experts: the router, the order
+ * of its tokens by expert and the way back, and the linear product with bias,
+ * activation and residual; each with its gradient.  The residual layer's
+ * conventions above hold.  What index arrays on the device hold is not checked
+ * by the host: entries outside their range are passed over as said below, and
+ * nothing outside the given arrays is read or written for them.
+ * ------------------------------------------------------------------------- */
+
+typedef enum {
+  SSM_SOFTMAX = 0,
+  SSM_SIGMOID = 1
+} ssm_score;
+
+/* Sizes of a router.  experts at most 1024; topk at most 16 and at most experts;
+ * tokens * topk at most 2^30. */
+typedef struct {
+  int64_t tokens;
+  int32_t experts;
+  int32_t topk;
+  int32_t score;         /* ssm_score */
+  int32_t renormalize;   /* nonzero: a token's weights are divided by their sum */
+  int32_t dtype;         /* ssm_dtype of logits, dlogits */
+} route_dims;
+
+/*
+ * Router: scores s_t = softmax(logits_t), or sigmoid of each, and the choice of
+ * topk experts.
+ *   logits    : [tokens][experts] of dtype
+ *   index     : [tokens][topk], the experts of the topk largest logits, largest
+ *               first, equal ones by number; a NaN counts as the lowest finite
+ *               value there.  An expert whose logit is -inf is not chosen: where
+ *               fewer than topk are left, -1.
+ *   weight    : [tokens][topk] float32, scale times the chosen experts' scores,
+ *               divided by their sum with renormalize; 0 where index is -1
+ *   score_sum : [experts] float32 (nullable), each expert's scores summed over the
+ *               tokens (a row of -inf adds nothing)
+ *   work      : expert_route_work_bytes(dims) bytes (nullable without score_sum)
+ */
+int64_t expert_route_work_bytes(const route_dims* dims);
+int expert_route_fwd(const void* logits, float scale, int32_t* index,
+                     float* weight, float* score_sum, void* work,
+                     const route_dims* dims, void* stream);
+
+/*
+ * Its gradient with respect to logits, of sum dweight*weight + sum
+ * dscore_sum*score_sum, with the choice held.
+ *   index      : as the forward wrote it (nullable without dweight); an entry
+ *                outside 0 .. experts - 1 takes no part
+ *   dweight    : [tokens][topk] float32 (nullable = zeros)
+ *   dscore_sum : [experts] float32 (nullable = zeros); one of the two is given
+ *   dlogits    : [tokens][experts] of dtype
+ */
+int expert_route_bwd(const void* logits, float scale, const int32_t* index,
+                     const float* dweight, const float* dscore_sum,
+                     void* dlogits, const route_dims* dims, void* stream);
+
+/*
+ * The order by expert: rows offsets[e] .. offsets[e + 1] - 1 are expert e's, in
+ * the order of (token, choice); limits as of route_dims, but topk may exceed
+ * experts (a token may name an expert twice).
+ *   index   : [tokens][topk]; an entry outside 0 .. experts - 1 has no row
+ *   offsets : [experts + 1]
+ *   token   : [tokens * topk], the token of every row; -1 past offsets[experts]
+ *   slot    : [tokens][topk], the row of every choice; -1 for one without
+ *   work    : expert_sort_work_bytes(tokens, topk, experts) bytes
+ */
+int64_t expert_sort_work_bytes(int64_t tokens, int32_t topk, int32_t experts);
+int expert_sort(const int32_t* index, int64_t tokens, int32_t topk,
+                int32_t experts, int32_t* offsets, int32_t* token,
+                int32_t* slot, void* work, void* stream);
+
+/* Sizes of the way into the order and back: rows of dim values. */
+typedef struct {
+  int64_t tokens;
+  int64_t rows;            /* of xs, y, dy; at most 2^30 */
+  int64_t dim;
+  int32_t topk;            /* at most 16 */
+  int32_t dtype;           /* ssm_dtype of x, xs, y, dy */
+  int32_t residual_dtype;  /* ssm_dtype of residual, out, dout */
+} order_dims;
+
+/* xs[r] = x[token[r]], zeros where that is no token: x [tokens][dim],
+ * token [rows], xs [rows][dim].  Its gradient is expert_combine_fwd without
+ * weights of the gradient of xs (dims->topk is not used here). */
+int expert_gather(const void* x, const int32_t* token, void* xs,
+                  const order_dims* dims, void* stream);
+
+/*
+ * out[t] = residual[t] + sum_j weight[t][j] y[slot[t][j]], summed in float32; a
+ * slot outside 0 .. rows - 1 adds nothing.
+ *   y : [rows][dim];  slot, weight : [tokens][topk] (weight nullable = 1)
+ *   residual, out : [tokens][dim] of residual_dtype (residual nullable; out may be
+ *   residual itself)
+ */
+int expert_combine_fwd(const void* y, const int32_t* slot, const float* weight,
+                       const void* residual, void* out, const order_dims* dims,
+                       void* stream);
+
+/*
+ * Its gradient: dy[slot[t][j]] = weight[t][j] dout[t], dweight[t][j] =
+ * dout[t].y[slot[t][j]], 0 for a slot outside the rows (the residual's is dout).
+ * A row may be in one slot only; one in no slot is left as it is.
+ *   dweight : [tokens][topk] float32 (nullable); needs y and weight
+ */
+int expert_combine_bwd(const void* dout, const void* y, const int32_t* slot,
+                       const float* weight, void* dy, float* dweight,
+                       const order_dims* dims, void* stream);
+
+typedef enum {
+  SSM_ACT_NONE = 0,
+  SSM_ACT_SILU = 1,    /* v sigmoid(v) */
+  SSM_ACT_GELU = 2,    /* v Phi(v), Phi the normal distribution function */
+  SSM_ACT_SWIGLU = 3,  /* silu(first half) * second half */
+  SSM_ACT_GEGLU = 4    /* gelu(first half) * second half */
+} ssm_activation;
+
+/* Sizes of a product: nw = n, or 2 n with a gated activation. */
+typedef struct {
+  int64_t rows;
+  int64_t n;            /* columns of out; a multiple of 8 */
+  int64_t k;            /* columns of x; a multiple of 8 */
+  int64_t x_rows;       /* rows of x: rows without token */
+  int64_t ld_x;         /* elements between x's rows, >= k, a multiple of 8 */
+  int32_t experts;      /* 0: one matrix for all rows; at most 1024 */
+  int32_t activation;   /* ssm_activation */
+  int32_t dtype;        /* ssm_dtype of x, w, pre, dx, dw */
+  int32_t out_dtype;    /* ssm_dtype of out, residual, dout */
+} product_dims;
+
+/*
+ * Linear product with bias, activation and residual, summed in float32:
+ *   pre[r][m] = sum_k x[r'][k] w[e][m][k] + bias[e][m],
+ *   out[r][c] = act(pre[r])[c] + residual[r][c],
+ * r' = token[r] (r without token; a row of zeros where that is none of x's), e the
+ * expert whose rows offsets[e] .. offsets[e + 1] - 1 hold r.
+ *   x        : [x_rows][k], row stride ld_x
+ *   token    : [rows] (nullable; only with experts)
+ *   w        : [experts][nw][k]  ([nw][k] with experts 0)
+ *   offsets  : [experts + 1], from 0, none less than the one before (NULL with
+ *              experts 0).  Rows from offsets[experts] on are left as they are.
+ *   bias     : [experts][nw] float32 (nullable)
+ *   residual : [rows][n] of out_dtype (nullable); out may be residual itself
+ *   out      : [rows][n] of out_dtype
+ *   pre      : [rows][nw] of dtype (nullable), what linear_bwd needs of an activation
+ *   work     : linear_fwd_work_bytes(dims) bytes
+ * Arrays of activations, weights and bias must be 16-byte aligned.
+ */
+int64_t linear_fwd_work_bytes(const product_dims* dims);
+int linear_fwd(const void* x, const int32_t* token, const void* w,
+               const int32_t* offsets, const float* bias, const void* residual,
+               void* out, void* pre, void* work, const product_dims* dims,
+               void* stream);
+
+#define SSM_WANT_DX 1
+#define SSM_WANT_DW 2
+#define SSM_WANT_DBIAS 4
+
+/*
+ * Its gradient (the residual's is dout):
+ *   dpre = act'(pre) dout,  dx[r] = dpre[r] w[e],  dw[e] = sum_r dpre[r] x[r'],
+ *   dbias[e] = sum_r dpre[r], r over the expert's rows.
+ *   pre   : as the forward wrote it; NULL without activation
+ *   dx    : [rows][k] of dtype (nullable), by row, not by token: with token its rows
+ *           are summed by expert_combine_fwd.  Rows past the last expert's are left
+ *           as they are.
+ *   dw    : as w (nullable);  dbias : [experts][nw] float32 (nullable); zeros for an
+ *           expert without rows
+ *   work  : linear_bwd_work_bytes(dims, the SSM_WANT_ bits of those given) bytes
+ * With an activation, or where out_dtype is not dtype, dpre is rounded to dtype in
+ * front of the products (dbias is summed before that).
+ */
+int64_t linear_bwd_work_bytes(const product_dims* dims, int32_t wants);
+int linear_bwd(const void* dout, const void* x, const int32_t* token,
+               const void* w, const int32_t* offsets, const void* pre, void* dx,
+               void* dw, float* dbias, void* work, const product_dims* dims,
+               void* stream);
+
 /* As ssm_check_device_errors, of the gated recurrence's carry waits. */
 int gated_check_device_errors(void* stream);
 

@@ -27,3 +27,15 @@ from .layer import (  # noqa: F401
     fp8_quantize_weight,
     fp8_linear,
 )
+from .feed_forward import (  # noqa: F401
+    expert_route_fwd,
+    expert_route_bwd,
+    expert_sort,
+    expert_gather,
+    expert_combine_fwd,
+    expert_combine_bwd,
+    expert_linear_fwd,
+    expert_linear_bwd,
+    linear_fwd,
+    linear_bwd,
+)

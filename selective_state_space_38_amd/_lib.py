@@ -19,6 +19,8 @@ EXPORTED_MICRO = ("ssm_micro_valu", "ssm_micro_stream")
 SSM_F32 = 0
 SSM_BF16 = 1
 
+SSM_WANT_DX, SSM_WANT_DW, SSM_WANT_DBIAS = 1, 2, 4
+
 SSM_BBAR_DELTA = 0
 SSM_BBAR_ZOH = 1
 
@@ -57,6 +59,18 @@ EXPORTED = (
     "fp8_quantize_weight",
     "fp8_linear_work_bytes",
     "fp8_linear",
+    "expert_route_work_bytes",
+    "expert_route_fwd",
+    "expert_route_bwd",
+    "expert_sort_work_bytes",
+    "expert_sort",
+    "expert_gather",
+    "expert_combine_fwd",
+    "expert_combine_bwd",
+    "linear_fwd_work_bytes",
+    "linear_fwd",
+    "linear_bwd_work_bytes",
+    "linear_bwd",
     "ssm_status_string",
     "ssm_check_device_errors",
     "gated_check_device_errors",
@@ -128,6 +142,42 @@ class LinearDims(ctypes.Structure):
         ("n", ctypes.c_int64),
         ("k", ctypes.c_int64),
         ("dtype", ctypes.c_int32),
+    ]
+
+
+class RouteDims(ctypes.Structure):
+    _fields_ = [
+        ("tokens", ctypes.c_int64),
+        ("experts", ctypes.c_int32),
+        ("topk", ctypes.c_int32),
+        ("score", ctypes.c_int32),
+        ("renormalize", ctypes.c_int32),
+        ("dtype", ctypes.c_int32),
+    ]
+
+
+class OrderDims(ctypes.Structure):
+    _fields_ = [
+        ("tokens", ctypes.c_int64),
+        ("rows", ctypes.c_int64),
+        ("dim", ctypes.c_int64),
+        ("topk", ctypes.c_int32),
+        ("dtype", ctypes.c_int32),
+        ("residual_dtype", ctypes.c_int32),
+    ]
+
+
+class ProductDims(ctypes.Structure):
+    _fields_ = [
+        ("rows", ctypes.c_int64),
+        ("n", ctypes.c_int64),
+        ("k", ctypes.c_int64),
+        ("x_rows", ctypes.c_int64),
+        ("ld_x", ctypes.c_int64),
+        ("experts", ctypes.c_int32),
+        ("activation", ctypes.c_int32),
+        ("dtype", ctypes.c_int32),
+        ("out_dtype", ctypes.c_int32),
     ]
 
 
@@ -249,6 +299,26 @@ def load():
             ("rms_norm_bwd", [vp] * 3 + [ctypes.c_float] + [vp] * 4 + [norm_p, vp]),
             ("fp8_quantize_weight", [vp, ctypes.c_int, i64, i64, vp, vp, vp]),
             ("fp8_linear", [vp] * 7 + [linear_p, vp])):
+        getattr(lib, name).argtypes = args
+        getattr(lib, name).restype = ctypes.c_int
+    route_p, order_p = ctypes.POINTER(RouteDims), ctypes.POINTER(OrderDims)
+    product_p, i32, f32 = ctypes.POINTER(ProductDims), ctypes.c_int32, ctypes.c_float
+    for name, args in (
+            ("expert_route_work_bytes", [route_p]),
+            ("expert_sort_work_bytes", [i64, i32, i32]),
+            ("linear_fwd_work_bytes", [product_p]),
+            ("linear_bwd_work_bytes", [product_p, i32])):
+        getattr(lib, name).argtypes = args
+        getattr(lib, name).restype = i64
+    for name, args in (
+            ("expert_route_fwd", [vp, f32] + [vp] * 4 + [route_p, vp]),
+            ("expert_route_bwd", [vp, f32] + [vp] * 4 + [route_p, vp]),
+            ("expert_sort", [vp, i64, i32, i32] + [vp] * 5),
+            ("expert_gather", [vp] * 3 + [order_p, vp]),
+            ("expert_combine_fwd", [vp] * 5 + [order_p, vp]),
+            ("expert_combine_bwd", [vp] * 6 + [order_p, vp]),
+            ("linear_fwd", [vp] * 9 + [product_p, vp]),
+            ("linear_bwd", [vp] * 10 + [product_p, vp])):
         getattr(lib, name).argtypes = args
         getattr(lib, name).restype = ctypes.c_int
     lib.ssm_status_string.argtypes = [ctypes.c_int]

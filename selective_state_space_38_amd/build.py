@@ -14,8 +14,8 @@ LIB = os.path.join(HERE, "libssm_scan.so")
 # the roofline ceiling probes: a library of their own, not part of the scan's ABI
 MICRO_LIB = os.path.join(HERE, "libssm_micro.so")
 MICRO_SOURCE = "micro.hip"
-# (source, object name, extra flags): the forward is compiled once per
-# activation type so the two halves build in parallel
+# (source, object name, extra flags): the forward and the linear product are
+# compiled once per activation type so the two halves build in parallel
 SOURCES = [
     ("api.hip", "api", []),
     ("scan_fwd.hip", "scan_fwd_f32", ["-DSSM_FWD_DTYPE=0"]),
@@ -29,6 +29,11 @@ SOURCES = [
     ("gated_scan.hip", "gated_scan", []),
     ("rms_norm.hip", "rms_norm", []),
     ("fp8_linear.hip", "fp8_linear", []),
+    ("feed_api.hip", "feed_api", []),
+    ("expert_route.hip", "expert_route", []),
+    ("expert_order.hip", "expert_order", []),
+    ("linear.hip", "linear_f32", ["-DSSM_LINEAR_DTYPE=0"]),
+    ("linear.hip", "linear_bf16", ["-DSSM_LINEAR_DTYPE=1"]),
 ]
 
 HIPCC_FLAGS = [
