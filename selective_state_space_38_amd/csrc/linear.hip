@@ -378,6 +378,25 @@ __device__ __forceinline__ int64_t tile_number(int64_t tiles) {
   return xcd * each + (xcd < more ? xcd : more) + bid / 8;
 }
 
+// kDw: `each` tiles for every expert, whose rows differ in number: the XCDs share each
+// expert's (one expert an XCD at a time left some idle: 950 us against 480 for 16 experts'
+// 16384 rows, 5120 x 2560).  Fewer than 16 tiles an expert go round as they come.
+__host__ __device__ __forceinline__ int64_t expert_grid(int64_t each, int64_t experts) {
+  return each < 16 ? each * experts : (each + 7) / 8 * 8 * experts;
+}
+__device__ __forceinline__ bool expert_tile(int64_t each, int64_t experts, int* expert, int64_t* t) {
+  const int64_t bid = blockIdx.x;
+  if (each < 16) {
+    *expert = static_cast<int>(bid / each);
+    *t = bid - *expert * each;
+    return *expert < experts;
+  }
+  const int64_t share = (each + 7) / 8, in = bid / 8;
+  *expert = static_cast<int>(in / share);
+  *t = bid % 8 * share + (in - *expert * share);
+  return *expert < experts && *t < each;
+}
+
 __device__ __forceinline__ void load4(const float* p, float (&v)[4]) {
   const f32x4 t = *reinterpret_cast<const f32x4*>(p);
 #pragma unroll
@@ -416,10 +435,9 @@ __global__ __launch_bounds__(64 * WN * WM, 2) void product_kernel(TileArgs p) {
   Range range = {0, p.rows};
   if constexpr (MODE == kDw) {
     const int64_t tiles_m = (p.high + BM - 1) / BM, each = tiles_m * tiles_n;
-    const int64_t t = tile_number(each * (p.offsets ? p.experts : 1));
-    if (t < 0) return;
-    expert = static_cast<int>(t / each);
-    place_of(t - expert * each, tiles_m, tiles_n, &tm, &tn);
+    int64_t t;
+    if (!expert_tile(each, p.offsets ? p.experts : 1, &expert, &t)) return;
+    place_of(t, tiles_m, tiles_n, &tm, &tn);
     range = rows_of(p.offsets, expert, p.rows);
     m0 = tm * BM;
     m_end = p.high;
@@ -490,6 +508,29 @@ __global__ __launch_bounds__(64 * WN * WM, 2) void product_kernel(TileArgs p) {
   for (int n = 0; n < NT; ++n)
 #pragma unroll
     for (int m = 0; m < MT; ++m) acc[n][m] = f32x4{};
+
+  // A wave without rows only loads its share of the operands: the other wave of its SIMD
+  // has the matrix instruction to itself (an expert's last tile).
+  if (MODE != kDw && m0 + wm * (BM / WM) >= m_end) {
+    if (groups > 0) {
+      load_a(s_a0, 0);
+      load_b(s_b0, 0);
+      __syncthreads();
+    }
+    if (groups > 1) {
+      load_a(s_a1, 1);
+      load_b(s_b1, 1);
+    }
+    for (int g = 0; g < groups; ++g) {
+      __syncthreads();
+      if (g + 2 < groups) {
+        load_a(g % 2 ? s_a1 : s_a0, g + 2);
+        load_b(g % 2 ? s_b1 : s_b0, g + 2);
+      }
+    }
+    __syncthreads();  // as the others do in front of their stores
+    return;
+  }
 
   if (groups > 0) {
     if constexpr (MODE == kDw) {
@@ -961,7 +1002,6 @@ struct Plan {
 
 constexpr int kStreamRows = 32;
 
-int side_of(int shape) { return shape == kTile256 ? 256 : shape == kTile128 ? 128 : 64; }
 
 // Most tiles of `side` rows that `rows` rows of the experts make: each expert's last
 // may be filled in part.
@@ -993,6 +1033,8 @@ Plan plan_tiles(const ProductArgs& a, int mode) {
   }
   if (parts > 0) q.parts = parts;
   if (q.parts > blocks) q.parts = static_cast<int>(blocks);
+  // with each = ceil(blocks / parts), drop the parts without a block
+  q.parts = static_cast<int>(div_up64(blocks, div_up64(blocks, q.parts)));
   return q;
 }
 
@@ -1008,21 +1050,21 @@ int64_t parts_bytes(const ProductArgs& a, int mode, const Plan& q) {
 }
 
 template <int MODE, int SIDE, int WN, int WM>
-void launch_side(const TileArgs& t, int64_t tiles_m, hipStream_t stream) {
+void launch_side(const TileArgs& t, hipStream_t stream) {
   constexpr int kCols = MODE == kGlu ? SIDE / 2 : SIDE;
-  const dim3 grid(static_cast<unsigned>(tiles_m * div_up64(t.cols, kCols)), t.parts);
+  const int experts = t.offsets ? t.experts : 0;
+  const int64_t tiles_n = div_up64(t.cols, kCols);
+  const int64_t tiles = MODE == kDw ? expert_grid(div_up64(t.high, SIDE) * tiles_n, experts ? experts : 1)
+                                    : most_tiles(t.rows, experts, SIDE) * tiles_n;
+  const dim3 grid(static_cast<unsigned>(tiles), t.parts);
   product_kernel<MODE, SIDE, SIDE, WN, WM><<<grid, 64 * WN * WM, 0, stream>>>(t);
 }
 
 template <int MODE>
 void launch_tiles(const TileArgs& t, int shape, hipStream_t stream) {
-  const int64_t side = side_of(shape);
-  const int experts = t.offsets ? t.experts : 0;
-  const int64_t tiles_m = MODE == kDw ? (experts ? experts : 1) * div_up64(t.high, side)
-                                      : most_tiles(t.rows, experts, side);
-  if (shape == kTile256) launch_side<MODE, 256, 2, 4>(t, tiles_m, stream);
-  else if (shape == kTile128) launch_side<MODE, 128, 2, 2>(t, tiles_m, stream);
-  else launch_side<MODE, 64, 2, 2>(t, tiles_m, stream);
+  if (shape == kTile256) launch_side<MODE, 256, 2, 4>(t, stream);
+  else if (shape == kTile128) launch_side<MODE, 128, 2, 2>(t, stream);
+  else launch_side<MODE, 64, 2, 2>(t, stream);
 }
 
 template <int MT>
