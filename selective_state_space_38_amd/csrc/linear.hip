@@ -414,10 +414,27 @@ __device__ __forceinline__ void store4(bf16_t* p, f32x4 v) {
   *reinterpret_cast<u32x2*>(p) = u32x2{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
 }
 
+// 8 values to p; STREAM: past the caches, which the operands need.
+template <bool STREAM, typename T>
+__device__ __forceinline__ void put8(T* p, const float (&v)[8]) {
+  if constexpr (!STREAM) {
+    store8(p, v);
+  } else if constexpr (sizeof(T) == 2) {
+    __builtin_nontemporal_store(u32x4{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]),
+                                      pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7])},
+                                reinterpret_cast<u32x4*>(p));
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; i += 4)
+      __builtin_nontemporal_store(f32x4{v[i], v[i + 1], v[i + 2], v[i + 3]}, reinterpret_cast<f32x4*>(p + i));
+  }
+}
+
 template <int MODE, int BN, int BM, int WN, int WM>
 __global__ __launch_bounds__(64 * WN * WM, 2) void product_kernel(TileArgs p) {
   constexpr int WAVES = WN * WM, NT = BN / WN / 16, MT = BM / WM / 16;
   constexpr bool GLU = MODE == kGlu, A_COL = MODE == kDx || MODE == kDw, B_COL = MODE == kDw;
+  constexpr bool STREAM = BM == 256;
   // separate objects, so that reads of one are known not to wait for loads into another
   __shared__ __align__(1024) uint8_t s_a0[BN * kBlockBytes];
   __shared__ __align__(1024) uint8_t s_a1[BN * kBlockBytes];
@@ -645,14 +662,14 @@ __global__ __launch_bounds__(64 * WN * WM, 2) void product_kernel(TileArgs p) {
       if constexpr (GLU) get(chunk + 4, u);
       if (p.parts > 1) {
         float* to = p.part + part * p.part_stride + (MODE == kDw ? expert * p.high + r : r) * width + col;
-        store8(to, v);
-        if constexpr (GLU) store8(to + p.cols, u);
+        put8<STREAM>(to, v);
+        if constexpr (GLU) put8<STREAM>(to + p.cols, u);
         continue;
       }
       if constexpr (MODE == kDx) {
-        store8(static_cast<Act*>(p.out) + r * p.cols + col, v);
+        put8<STREAM>(static_cast<Act*>(p.out) + r * p.cols + col, v);
       } else if constexpr (MODE == kDw) {
-        store8(static_cast<Act*>(p.out) + (expert * p.high + r) * p.cols + col, v);
+        put8<STREAM>(static_cast<Act*>(p.out) + (expert * p.high + r) * p.cols + col, v);
       } else {
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
@@ -660,8 +677,8 @@ __global__ __launch_bounds__(64 * WN * WM, 2) void product_kernel(TileArgs p) {
           if constexpr (GLU) u[e] += bias[1][e];
         }
         if (p.pre) {
-          store8(static_cast<Act*>(p.pre) + r * width + col, v);
-          if constexpr (GLU) store8(static_cast<Act*>(p.pre) + r * width + p.cols + col, u);
+          put8<STREAM>(static_cast<Act*>(p.pre) + r * width + col, v);
+          if constexpr (GLU) put8<STREAM>(static_cast<Act*>(p.pre) + r * width + p.cols + col, u);
         }
         if (is_silu(p.act)) {
 #pragma unroll
@@ -687,8 +704,8 @@ __global__ __launch_bounds__(64 * WN * WM, 2) void product_kernel(TileArgs p) {
             for (int e = 0; e < 8; ++e) v[e] += t.get(e);
           }
         }
-        if (p.out_f32) store8(static_cast<float*>(p.out) + r * p.cols + col, v);
-        else store8(static_cast<bf16_t*>(p.out) + r * p.cols + col, v);
+        if (p.out_f32) put8<STREAM>(static_cast<float*>(p.out) + r * p.cols + col, v);
+        else put8<STREAM>(static_cast<bf16_t*>(p.out) + r * p.cols + col, v);
       }
     }
   }
