@@ -20,6 +20,7 @@ template <typename T, int L, int V>
 struct Scores {
   float x[V], s[V];  // logits (past the row's end: -inf), scores
   int first;         // the lane's first expert
+  float base, scale; // softmax: s = exp(x - base) scale
 
   __device__ __forceinline__ static float all_max(float v) {
     v = row16_max(v);
@@ -60,15 +61,19 @@ struct Scores {
 #pragma unroll
     for (int v = 1; v < V; ++v) top = fmaxf(top, x[v]);
     top = all_max(top);
-    const float base = top == -__builtin_inff() ? 0.0f : top;  // a row without an expert
+    base = top == -__builtin_inff() ? 0.0f : top;  // a row without an expert
 #pragma unroll
     for (int v = 0; v < V; ++v) sum += s[v] = exp2_hw((x[v] - base) * kLog2e);
     sum = all_sum(sum);
-    const float scale = sum == 0.0f ? 0.0f : 1.0f / sum;
+    scale = sum == 0.0f ? 0.0f : 1.0f / sum;
 #pragma unroll
     for (int v = 0; v < V; ++v) s[v] *= scale;
   }
 
+  // the score of logit x
+  __device__ __forceinline__ float score_of(float x, bool sigmoid) const {
+    return sigmoid ? sigmoid_of(x) : exp2_hw((x - base) * kLog2e) * scale;
+  }
   __device__ __forceinline__ static float sigmoid_of(float x) {
     return 1.0f / (1.0f + exp2_hw(-x * kLog2e));
   }
@@ -84,6 +89,7 @@ struct Scores {
 };
 
 constexpr int kRouteThreads = 256;
+constexpr float kLowest = -3.402823466e38f;  // the lowest finite value
 
 template <typename T, int L, int V>
 __global__ __launch_bounds__(kRouteThreads) void route_fwd_kernel(RouteArgs p) {
@@ -106,28 +112,35 @@ __global__ __launch_bounds__(kRouteThreads) void route_fwd_kernel(RouteArgs p) {
     }
     float key[V];
 #pragma unroll
-    for (int v = 0; v < V; ++v) key[v] = r.x[v] != r.x[v] ? -3.402823466e38f : r.x[v];
+    for (int v = 0; v < V; ++v) key[v] = r.x[v] != r.x[v] ? kLowest : r.x[v];
     float mine = 0.0f, sum = 0.0f, top = 0.0f;  // choice `at`'s weight; lanes 0 .. K - 1
     int chosen = -1;
     for (int j = 0; j < K; ++j) {
-      float best = key[0], x = r.x[0], s = r.s[0];
-      int v_of = 0;
+      float m = key[0];
 #pragma unroll
-      for (int v = 1; v < V; ++v)
-        if (key[v] > best) best = key[v], x = r.x[v], s = r.s[v], v_of = v;
-      const float m = S::all_max(best);
+      for (int v = 1; v < V; ++v) m = fmaxf(m, key[v]);
+      m = S::all_max(m);
       if (m == -__builtin_inff()) break;
-      const uint64_t hit = __ballot(best == m) >> (group * L) & (L == 64 ? ~0ull : 0xffffull);
+      int v_of = -1;  // the lane's first of them
+#pragma unroll
+      for (int v = V - 1; v >= 0; --v) v_of = key[v] == m ? v : v_of;
+      const uint64_t hit = __ballot(v_of >= 0) >> (group * L) & (L == 64 ? ~0ull : 0xffffull);
       const int who = __builtin_ctzll(hit);
+      const int e = __shfl(r.first + v_of, group * L + who);
       if (at == who) {
 #pragma unroll
-        for (int v = 0; v < V; ++v)
-          if (v == v_of) key[v] = -__builtin_inff();
+        for (int v = 0; v < V; ++v) key[v] = v == v_of ? -__builtin_inff() : key[v];
       }
-      x = __shfl(x, group * L + who);
-      const int e = __shfl(r.first + v_of, group * L + who);
+      // its logit is m but for a NaN that counts as the lowest
+      float x = m;
+      if (m == kLowest) {
+        float own = 0.0f;
+#pragma unroll
+        for (int v = 0; v < V; ++v) own = v == v_of ? r.x[v] : own;
+        x = __shfl(own, group * L + who);
+      }
       if (j == 0) top = x;
-      s = p.renormalize ? S::share(x, top, p.sigmoid) : __shfl(s, group * L + who);
+      const float s = p.renormalize ? S::share(x, top, p.sigmoid) : r.score_of(x, p.sigmoid);
       sum += s;
       if (at == j) mine = s, chosen = e;
     }
@@ -360,10 +373,11 @@ __global__ __launch_bounds__(256) void sort_scan_kernel(int* counts, int groups,
 template <int ROUNDS>
 __global__ __launch_bounds__(64 * kSortWaves) void sort_place_kernel(SortArgs p, int64_t entries,
                                                                      int bits, bool scanned) {
-  extern __shared__ int lds[];  // first place [E + 1], sums [waves], counters [waves][E + 1]
+  extern __shared__ int lds[];  // first place [E + 1], totals [E + 1], sums [waves], counters [waves][E + 1]
   const int bins = p.experts + 1;
   int* place = lds;
-  int* sums = place + bins;
+  int* s_total = place + bins;
+  int* sums = s_total + bins;
   uint16_t* counters = reinterpret_cast<uint16_t*>(sums + kSortWaves);
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   for (int e = threadIdx.x; e < kSortWaves * bins; e += blockDim.x) counters[e] = 0;
@@ -410,14 +424,32 @@ __global__ __launch_bounds__(64 * kSortWaves) void sort_place_kernel(SortArgs p,
     }
     if (e == 0) missing = counts[static_cast<int64_t>(mine) * bins + p.experts];
   } else if (groups > 1) {
-    total = 0;
-    for (int g = 0; g < groups; ++g) {
-      const int c = e < bins ? counts[g * bins + e] : 0;
-      if (g < mine) earlier += c;
-      total += c;
+    // 1024 / span threads a bin, each every so many-th workgroup's count
+    int span = 64;
+    while (span < bins) span *= 2;
+    if (span > blockDim.x) span = blockDim.x;  // the last bin (none) is thread 0's below
+    const int stride = blockDim.x / span, bin0 = e % span;
+    int all = 0, ahead = 0;
+#pragma unroll 8
+    for (int g = e / span; g < groups; g += stride) {
+      const int c = bin0 < bins ? counts[g * bins + bin0] : 0;
+      ahead += g < mine ? c : 0;
+      all += c;
     }
-    if (e == 0)
-      for (int g = 0; g < mine; ++g) missing += counts[g * bins + p.experts];
+    for (int b = e; b < bins; b += blockDim.x) place[b] = s_total[b] = 0;
+    __syncthreads();
+    if (bin0 < bins) {
+      atomicAdd(&s_total[bin0], all);  // whole numbers: any order
+      atomicAdd(&place[bin0], ahead);
+    }
+    __syncthreads();
+    total = e < bins ? s_total[e] : 0;
+    earlier = e < bins ? place[e] : 0;
+    if (e == 0) {
+      missing = p.experts < span ? place[p.experts] : 0;
+      for (int g = 0; g < mine && p.experts >= span; ++g) missing += counts[g * bins + p.experts];
+    }
+    __syncthreads();
   }
   // exclusive sums over the experts (the bin of pairs without one starts where the
   // experts' end)
@@ -479,7 +511,7 @@ static void launch_sort_rounds(const SortArgs& a, int64_t entries, hipStream_t s
     sort_scan_kernel<<<bins, 256, 0, stream>>>(static_cast<int*>(a.work), static_cast<int>(groups),
                                                bins);
   sort_place_kernel<ROUNDS>
-      <<<grid, 64 * kSortWaves, (bins + kSortWaves) * 4 + kSortWaves * bins * 2, stream>>>(
+      <<<grid, 64 * kSortWaves, (2 * bins + kSortWaves) * 4 + kSortWaves * bins * 2, stream>>>(
           a, entries, bits, groups > kSortDirect);
 }
 

@@ -780,10 +780,12 @@ __global__ __launch_bounds__(256) void join_kernel(JoinArgs p) {
 // matrix (of a gated one 16 of either half), its waves the blocks of 128 bytes in
 // turn; the activations come from the L2.  The waves' sums meet in LDS and are added
 // in wave order.  A matrix with more than 16 MT rows is read again for the next ones.
+constexpr int kStreamWaves = 8;
+
 template <int MT, bool GLU>
-__global__ __launch_bounds__(1024) void stream_kernel(TileArgs p) {
+__global__ __launch_bounds__(64 * kStreamWaves) void stream_kernel(TileArgs p) {
   constexpr int H = GLU ? 2 : 1;
-  __shared__ f32x4 s_sum[16][H * MT][64];
+  __shared__ f32x4 s_sum[kStreamWaves][H * MT][64];
   const int lane = threadIdx.x & 63, i = lane & 15, quad = lane >> 4;
   const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int W = blockDim.x >> 6;
@@ -813,14 +815,15 @@ __global__ __launch_bounds__(1024) void stream_kernel(TileArgs p) {
               (expert * p.stride_a + (c_lane + h * p.cols) * p.lda) * kSize;
   const int bytes = static_cast<int>(p.depth) * kSize;
   const int groups = (bytes + kBlockBytes - 1) / kBlockBytes;
+  // the quad's 16 bytes of either half of a row's 128: 64 bytes a row by one access
   auto load32 = [&](const char* row, int at) {
     i32x8 v = {};
     if (at < bytes) {
       const int4 t = *reinterpret_cast<const int4*>(row + at);
       v[0] = t.x; v[1] = t.y; v[2] = t.z; v[3] = t.w;
     }
-    if (at + 16 < bytes) {
-      const int4 t = *reinterpret_cast<const int4*>(row + at + 16);
+    if (at + 64 < bytes) {
+      const int4 t = *reinterpret_cast<const int4*>(row + at + 64);
       v[4] = t.x; v[5] = t.y; v[6] = t.z; v[7] = t.w;
     }
     return v;
@@ -840,12 +843,12 @@ __global__ __launch_bounds__(1024) void stream_kernel(TileArgs p) {
       xrow[m] = static_cast<const char*>(p.b) + (in[m] ? t : 0) * p.ldb * kSize;
     }
     f32x4 acc[H][MT] = {};
-    constexpr int U = 2;  // blocks in flight
+    constexpr int U = MT * H == 1 ? 4 : MT * H == 2 ? 3 : 2;  // blocks in flight
     for (int g0 = w; g0 < groups; g0 += U * W) {
       i32x8 a[U][H], b[U][MT];
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        const int at = (g0 + u * W) * kBlockBytes + quad * 32;
+        const int at = (g0 + u * W) * kBlockBytes + quad * 16;
 #pragma unroll
         for (int h = 0; h < H; ++h) a[u][h] = load32(wrow[h], at);
 #pragma unroll
@@ -902,29 +905,31 @@ __global__ __launch_bounds__(1024) void stream_kernel(TileArgs p) {
 // ---- backward: the activation's gradient and the bias' ----
 //
 // dpre in the activations' type for the two products, and its sums over the rows of
-// each tile of kBendRows of an expert from the values before that rounding.  A wave
+// each tile of p.tile rows of an expert from the values before that rounding.  A wave
 // takes 512 columns, 8 a lane, of every fourth row.
-constexpr int kBendRows = 128;
 
 struct BendArgs {
   const void *dout, *pre;
   void* dpre;               // nullable: dout serves as it is
   float* part;              // [tiles][nw], nullable
   const int32_t* offsets;
-  int experts, act;
+  int experts, act, tile;
   int64_t rows, n, max_tiles;
 };
+
+// Rows of a tile: few where that leaves the CUs without work.
+int bend_rows(int64_t rows, int64_t n) { return rows * n < (1 << 23) ? 32 : 128; }
 
 template <typename D>
 __global__ __launch_bounds__(256) void bend_kernel(BendArgs p) {
   __shared__ float s_part[4][64][17];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const Tiles tiles = {p.offsets, p.experts, p.rows, kBendRows};
+  const Tiles tiles = {p.offsets, p.experts, p.rows, p.tile};
   int expert, at;
   if (!tiles.find(static_cast<int>(blockIdx.x), &expert, &at)) return;
   const Range range = rows_of(p.offsets, expert, p.rows);
-  const int64_t m0 = range.from + static_cast<int64_t>(at) * kBendRows;
-  const int64_t m_end = m0 + kBendRows < range.to ? m0 + kBendRows : range.to;
+  const int64_t m0 = range.from + static_cast<int64_t>(at) * p.tile;
+  const int64_t m_end = m0 + p.tile < range.to ? m0 + p.tile : range.to;
   const int64_t c = static_cast<int64_t>(blockIdx.y) * 512 + lane * 8;
   const bool live = c < p.n, glu = is_gated(p.act);
   const int64_t width = glu ? 2 * p.n : p.n;
@@ -977,15 +982,15 @@ __global__ __launch_bounds__(256) void bend_kernel(BendArgs p) {
   }
 }
 
-// dbias[e] = the sum of the expert's tiles, 64 columns a workgroup, each wave a
-// fourth of the tiles in turn.
-__global__ __launch_bounds__(256) void bias_kernel(BendArgs p, float* dbias) {
-  __shared__ float s_part[4][64];
+// dbias[e] = the sum of the expert's tiles, 64 columns a workgroup, its waves
+// the tiles in turn.
+__global__ __launch_bounds__(1024) void bias_kernel(BendArgs p, float* dbias) {
+  __shared__ float s_part[16][64];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int expert = blockIdx.y;
   const int64_t width = is_gated(p.act) ? 2 * p.n : p.n, c = static_cast<int64_t>(blockIdx.x) * 64 + lane;
-  const Tiles tiles = {p.offsets, p.experts, p.rows, kBendRows};
-  int64_t from = 0, count = (p.rows + kBendRows - 1) / kBendRows;
+  const Tiles tiles = {p.offsets, p.experts, p.rows, p.tile};
+  int64_t from = 0, count = (p.rows + p.tile - 1) / p.tile;
   if (p.offsets) {
     count = tiles.count(expert);
     for (int e0 = 0; e0 < expert; e0 += 64) {
@@ -996,12 +1001,16 @@ __global__ __launch_bounds__(256) void bias_kernel(BendArgs p, float* dbias) {
   }
   float sum = 0.0f;
   if (c < width)
-    for (int64_t t = from + wave; t < from + count; t += 4) sum += p.part[t * width + c];
+#pragma unroll 4
+    for (int64_t t = from + wave; t < from + count; t += 16) sum += p.part[t * width + c];
   s_part[wave][lane] = sum;
   __syncthreads();
-  if (wave == 0 && c < width)
-    dbias[expert * width + c] =
-        (s_part[0][lane] + s_part[1][lane]) + (s_part[2][lane] + s_part[3][lane]);
+  if (wave == 0 && c < width) {
+    sum = 0.0f;
+#pragma unroll
+    for (int w = 0; w < 16; ++w) sum += s_part[w][lane];
+    dbias[expert * width + c] = sum;
+  }
 }
 
 // ---- plans ----
@@ -1018,6 +1027,7 @@ struct Plan {
 };
 
 constexpr int kStreamRows = 32;
+constexpr int64_t kCus = 256;
 
 
 // Most tiles of `side` rows that `rows` rows of the experts make: each expert's last
@@ -1045,8 +1055,19 @@ Plan plan_tiles(const ProductArgs& a, int mode) {
   if (q.shape == kStream) return q;
   const int64_t blocks = div_up64(depth, kBlock);
   if (q.shape == kTile64) {
-    const int64_t t = tiles(64);
-    while (q.parts < 8 && t * q.parts * 2 <= 512 && blocks / (q.parts * 2) >= 4) q.parts *= 2;
+    // a block takes 0.42 us, of float32 on every CU, of bfloat16 three workgroups a CU
+    // at a time; the join 4 us and its traffic, written and read at 2.5 TB/s
+    const int64_t slots = kSize == 4 ? kCus : 3 * kCus;
+    const double values = static_cast<double>(matrices) * high * cols;
+    double best = 0.0;
+    for (int t = 1; t <= 8 && t <= blocks; ++t) {
+      const double rounds = static_cast<double>(div_up64(tiles(64) * t, slots));
+      const double us = 0.42 * rounds * div_up64(blocks, t) + (t > 1 ? 4.0 + 8e-6 / 2.5 * values * t : 0.0);
+      if (t == 1 || us < best) {
+        best = us;
+        q.parts = t;
+      }
+    }
   }
   if (parts > 0) q.parts = parts;
   if (q.parts > blocks) q.parts = static_cast<int>(blocks);
@@ -1087,7 +1108,7 @@ void launch_tiles(const TileArgs& t, int shape, hipStream_t stream) {
 template <int MT>
 void launch_stream(const TileArgs& t, bool glu, hipStream_t stream) {
   const int64_t groups = div_up64(t.depth * kSize, kBlockBytes);
-  const int waves = static_cast<int>(div_up64(groups, div_up64(groups, 16)));
+  const int waves = static_cast<int>(div_up64(groups, div_up64(groups, kStreamWaves)));
   const int64_t y = !t.offsets ? 1 : t.rows < t.experts ? t.rows : t.experts;
   const dim3 grid(static_cast<unsigned>(div_up64(t.cols, 16)), static_cast<unsigned>(y));
   if (glu) stream_kernel<MT, true><<<grid, 64 * waves, 0, stream>>>(t);
@@ -1125,7 +1146,7 @@ BwdLayout bwd_layout(const ProductArgs& a) {
   const bool copy = a.act != kNoAct || a.out_dtype != a.dtype;
   l.bend = copy || a.dbias;
   l.dpre = copy ? up16(a.rows * a.nw() * kSize) : 0;
-  l.tiles = most_tiles(a.rows, a.experts, kBendRows);
+  l.tiles = most_tiles(a.rows, a.experts, bend_rows(a.rows, a.n));
   l.bias = a.dbias ? up16(l.tiles * a.nw() * 4) : 0;
   if (a.dx) {
     l.dx = plan_tiles(a, kDx);
@@ -1181,7 +1202,8 @@ hipError_t SSM_TYPED(launch_product_fwd)(const ProductArgs& a, hipStream_t strea
   t.part = static_cast<float*>(a.work);
   t.part_stride = a.rows * a.nw();
   if (q.shape == kStream) {
-    if (a.rows <= 16) launch_stream<1>(t, glu, stream);
+    // (the fewest rows that any matrix can have to be sure; of experts' the mean is far below)
+    if (a.rows <= (a.experts > 2 ? 8 * a.experts : 16)) launch_stream<1>(t, glu, stream);
     else launch_stream<2>(t, glu, stream);
   } else {
     if (glu) launch_tiles<kGlu>(t, q.shape, stream);
@@ -1206,6 +1228,7 @@ hipError_t SSM_TYPED(launch_product_bwd)(const ProductArgs& a, hipStream_t strea
     b.offsets = offsets;
     b.experts = a.experts;
     b.act = a.act;
+    b.tile = bend_rows(a.rows, a.n);
     b.rows = a.rows;
     b.n = a.n;
     b.max_tiles = l.tiles;
@@ -1214,7 +1237,7 @@ hipError_t SSM_TYPED(launch_product_bwd)(const ProductArgs& a, hipStream_t strea
     else bend_kernel<bf16_t><<<grid, 256, 0, stream>>>(b);
     if (l.bias) {
       const dim3 sums(static_cast<unsigned>(div_up64(nw, 64)), a.experts ? a.experts : 1);
-      bias_kernel<<<sums, 256, 0, stream>>>(b, a.dbias);
+      bias_kernel<<<sums, 1024, 0, stream>>>(b, a.dbias);
     }
     if (l.dpre) dpre = work;
   }
