@@ -55,7 +55,7 @@ __global__ __launch_bounds__(kOrderThreads) void gather_kernel(OrderArgs p) {
   const bool in = t >= 0 && t < p.tokens;
   const T* from = static_cast<const T*>(p.x) + (in ? t : 0) * p.dim;
   T* to = static_cast<T*>(p.xs) + r * p.dim;
-  constexpr int U = 4;
+  constexpr int U = 8 * 2 / sizeof(T);  // runs in flight
   for (int c0 = at; c0 < runs; c0 += U * L) {
     Run8<T> v[U];
 #pragma unroll
@@ -72,34 +72,42 @@ __global__ __launch_bounds__(kOrderThreads) void gather_kernel(OrderArgs p) {
   }
 }
 
-// A token's rows are found once: lane j < topk holds choice j's.
-template <typename T, typename R, int L>
+// K: topk, rounded up.  A run of all of a token's rows is read before the first is added.
+template <typename T, typename R, int L, int K>
 __global__ __launch_bounds__(kOrderThreads) void combine_kernel(OrderArgs p) {
   const int64_t t = static_cast<int64_t>(blockIdx.x) * (kOrderThreads / L) + threadIdx.x / L;
   if (t >= p.tokens) return;
   const int at = threadIdx.x & (L - 1);
   const int dim = static_cast<int>(p.dim), runs = (dim + 7) / 8;
-  const int32_t* slot = p.slot + t * p.topk;
-  const T* y = static_cast<const T*>(p.y);
+  const T* from[K];
+  float w[K];
+#pragma unroll
+  for (int j = 0; j < K; ++j) {
+    const int64_t r = j < p.topk ? p.slot[t * p.topk + j] : -1;
+    const bool in = r >= 0 && r < p.rows;
+    w[j] = in && p.weight ? p.weight[t * p.topk + j] : 1.0f;
+    from[j] = in ? static_cast<const T*>(p.y) + r * p.dim : nullptr;
+  }
   R* to = static_cast<R*>(p.out) + t * p.dim;
-  const R* res = static_cast<const R*>(p.residual) + t * p.dim;
+  const R* res = p.residual ? static_cast<const R*>(p.residual) + t * p.dim : nullptr;
   for (int c = at; c < runs; c += L) {
     const int left = dim - 8 * c;
+    Run8<T> v[K];
+    Run8<R> q;
+#pragma unroll
+    for (int j = 0; j < K; ++j)
+      if (from[j]) load8<T, false>(v[j], from[j] + 8 * c, left);
+    if (res) load8<R, false>(q, res + 8 * c, left);
     float sum[8] = {};
-    for (int j = 0; j < p.topk; ++j) {
-      const int64_t r = slot[j];
-      if (r < 0 || r >= p.rows) continue;
-      const float w = p.weight ? p.weight[t * p.topk + j] : 1.0f;
-      Run8<T> v;
-      load8<T, false>(v, y + r * p.dim + 8 * c, left);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) sum[e] = fmaf(w, v.get(e), sum[e]);
-    }
-    if (p.residual) {
-      Run8<R> v;
-      load8<R, false>(v, res + 8 * c, left);
+    for (int j = 0; j < K; ++j)
+      if (from[j]) {
 #pragma unroll
-      for (int e = 0; e < 8; ++e) sum[e] += v.get(e);
+        for (int e = 0; e < 8; ++e) sum[e] = fmaf(w[j], v[j].get(e), sum[e]);
+      }
+    if (res) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) sum[e] += q.get(e);
     }
     store8(to + 8 * c, sum, left < 8 ? left - 1 : 7);
   }
@@ -134,21 +142,23 @@ __global__ __launch_bounds__(kOrderThreads) void combine_bwd_kernel(OrderArgs p)
   for (int c = at; c < runs; c += L) {
     const int left = dim - 8 * c, last = left < 8 ? left - 1 : 7;
     Run8<R> d;
+    Run8<T> v[K];
     load8<R, false>(d, dout + 8 * c, left);
+#pragma unroll
+    for (int j = 0; j < K; ++j)
+      if (p.dweight && row[j] >= 0) load8<T, false>(v[j], y + row[j] * p.dim + 8 * c, left);
 #pragma unroll
     for (int j = 0; j < K; ++j) {
       if (row[j] < 0) continue;
-      if (p.dweight) {
-        Run8<T> v;
-        load8<T, false>(v, y + row[j] * p.dim + 8 * c, left);
-#pragma unroll
-        for (int e = 0; e < 8; ++e)
-          dot[j] = fmaf(e <= last ? d.get(e) : 0.0f, e <= last ? v.get(e) : 0.0f, dot[j]);
-      }
       float g[8];
 #pragma unroll
       for (int e = 0; e < 8; ++e) g[e] = w[j] * d.get(e);
       store8(dy + row[j] * p.dim + 8 * c, g, last);
+      if (p.dweight) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          dot[j] = fmaf(e <= last ? d.get(e) : 0.0f, e <= last ? v[j].get(e) : 0.0f, dot[j]);
+      }
     }
   }
   if (!p.dweight) return;
@@ -173,12 +183,21 @@ static void launch_gather_typed(const OrderArgs& a, hipStream_t stream) {
     gather_kernel<T, 64><<<order_grid(a.rows, 64), kOrderThreads, 0, stream>>>(a);
 }
 
+template <typename T, typename R, int K>
+static void launch_combine_k(const OrderArgs& a, hipStream_t stream) {
+  if (narrow(a.dim))
+    combine_kernel<T, R, 16, K><<<order_grid(a.tokens, 16), kOrderThreads, 0, stream>>>(a);
+  else
+    combine_kernel<T, R, 64, K><<<order_grid(a.tokens, 64), kOrderThreads, 0, stream>>>(a);
+}
+
 template <typename T, typename R>
 static void launch_combine_typed(const OrderArgs& a, hipStream_t stream) {
-  if (narrow(a.dim))
-    combine_kernel<T, R, 16><<<order_grid(a.tokens, 16), kOrderThreads, 0, stream>>>(a);
-  else
-    combine_kernel<T, R, 64><<<order_grid(a.tokens, 64), kOrderThreads, 0, stream>>>(a);
+  if (a.topk <= 1) launch_combine_k<T, R, 1>(a, stream);
+  else if (a.topk <= 2) launch_combine_k<T, R, 2>(a, stream);
+  else if (a.topk <= 4) launch_combine_k<T, R, 4>(a, stream);
+  else if (a.topk <= 8) launch_combine_k<T, R, 8>(a, stream);
+  else launch_combine_k<T, R, 16>(a, stream);
 }
 
 template <typename T, typename R, int K>
