@@ -772,7 +772,7 @@ typedef enum {
 /* Sizes of a product: nw = n, or 2 n with a gated activation. */
 typedef struct {
   int64_t rows;
-  int64_t n;            /* columns of out; a multiple of 8 */
+  int64_t n;            /* columns of out */
   int64_t k;            /* columns of x; a multiple of 8 */
   int64_t x_rows;       /* rows of x: rows without token */
   int64_t ld_x;         /* elements between x's rows, >= k, a multiple of 8 */
@@ -798,7 +798,8 @@ typedef struct {
  *   out      : [rows][n] of out_dtype
  *   pre      : [rows][nw] of dtype (nullable), what linear_bwd needs of an activation
  *   work     : linear_fwd_work_bytes(dims) bytes
- * Arrays of activations, weights and bias must be 16-byte aligned.
+ * Arrays of activations, weights and bias must be 16-byte aligned (their rows need not
+ * be, but x's and w's are, k and ld_x being multiples of 8).
  */
 int64_t linear_fwd_work_bytes(const product_dims* dims);
 int linear_fwd(const void* x, const int32_t* token, const void* w,

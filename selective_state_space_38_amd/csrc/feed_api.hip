@@ -86,7 +86,7 @@ int check_product(const product_dims* d) {
   if (!valid_dtype(d->dtype) || !valid_dtype(d->out_dtype)) return SSM_EDTYPE;
   if (d->activation < SSM_ACT_NONE || d->activation > SSM_ACT_GEGLU) return SSM_EINVAL;
   if (d->experts < 0 || d->experts > ssm::kMaxExperts) return SSM_EINVAL;
-  if (d->rows <= 0 || d->n <= 0 || d->k <= 0 || d->n % 8 || d->k % 8 || d->x_rows <= 0)
+  if (d->rows <= 0 || d->n <= 0 || d->k <= 0 || d->k % 8 || d->x_rows <= 0)
     return SSM_EINVAL;
   if (d->ld_x < d->k || d->ld_x > (1LL << 26) || d->ld_x % 8) return SSM_EINVAL;
   // limits of the launch arithmetic: 32-bit row numbers and counts of tiles

@@ -397,36 +397,59 @@ __device__ __forceinline__ bool expert_tile(int64_t each, int64_t experts, int* 
   return *expert < experts && *t < each;
 }
 
-__device__ __forceinline__ void load4(const float* p, float (&v)[4]) {
-  const f32x4 t = *reinterpret_cast<const f32x4*>(p);
+typedef u32x2 u32x2_any __attribute__((aligned(2)));
+
+// 4 values, of which those past `last` are not there: loaded as the last one, not stored.
+__device__ __forceinline__ f32x4 load4(const float* p, int last) {
+  if (last >= 3) {
+    const u32x4 t = *reinterpret_cast<const u32x4_any*>(p);
+    return f32x4{__uint_as_float(t[0]), __uint_as_float(t[1]), __uint_as_float(t[2]), __uint_as_float(t[3])};
+  }
+  return f32x4{p[0], p[last < 1 ? last : 1], p[last < 2 ? last : 2], p[last]};
+}
+__device__ __forceinline__ f32x4 load4(const bf16_t* p, int last) {
+  if (last >= 3) {
+    const u32x2 t = *reinterpret_cast<const u32x2_any*>(p);
+    return f32x4{__uint_as_float(t[0] << 16), __uint_as_float(t[0] & 0xffff0000u),
+                 __uint_as_float(t[1] << 16), __uint_as_float(t[1] & 0xffff0000u)};
+  }
+  return f32x4{to_f32(p[0]), to_f32(p[last < 1 ? last : 1]), to_f32(p[last < 2 ? last : 2]), to_f32(p[last])};
+}
+__device__ __forceinline__ void store4(float* p, f32x4 v, int last) {
+  if (last >= 3) {
+    *reinterpret_cast<u32x4_any*>(p) = u32x4{__float_as_uint(v[0]), __float_as_uint(v[1]),
+                                             __float_as_uint(v[2]), __float_as_uint(v[3])};
+    return;
+  }
 #pragma unroll
-  for (int j = 0; j < 4; ++j) v[j] = t[j];
+  for (int j = 0; j < 3; ++j)
+    if (j <= last) p[j] = v[j];
 }
-__device__ __forceinline__ void load4(const bf16_t* p, float (&v)[4]) {
-  const u32x2 t = *reinterpret_cast<const u32x2*>(p);
-  v[0] = __uint_as_float(t[0] << 16);
-  v[1] = __uint_as_float(t[0] & 0xffff0000u);
-  v[2] = __uint_as_float(t[1] << 16);
-  v[3] = __uint_as_float(t[1] & 0xffff0000u);
-}
-__device__ __forceinline__ void store4(float* p, f32x4 v) { *reinterpret_cast<f32x4*>(p) = v; }
-__device__ __forceinline__ void store4(bf16_t* p, f32x4 v) {
-  *reinterpret_cast<u32x2*>(p) = u32x2{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
+__device__ __forceinline__ void store4(bf16_t* p, f32x4 v, int last) {
+  if (last >= 3) {
+    *reinterpret_cast<u32x2_any*>(p) = u32x2{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
+    return;
+  }
+#pragma unroll
+  for (int j = 0; j < 3; ++j)
+    if (j <= last) store_act(p, j, v[j]);
 }
 
-// 8 values to p; STREAM: past the caches, which the operands need.
+// Values 0 .. last of 8 to p; STREAM: past the caches, which the operands need.
 template <bool STREAM, typename T>
-__device__ __forceinline__ void put8(T* p, const float (&v)[8]) {
-  if constexpr (!STREAM) {
-    store8(p, v);
+__device__ __forceinline__ void put8(T* p, const float (&v)[8], int last = 7) {
+  if (!STREAM || last < 7) {
+    store8(p, v, last);
   } else if constexpr (sizeof(T) == 2) {
     __builtin_nontemporal_store(u32x4{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]),
                                       pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7])},
-                                reinterpret_cast<u32x4*>(p));
+                                reinterpret_cast<u32x4_any*>(p));
   } else {
 #pragma unroll
     for (int i = 0; i < 8; i += 4)
-      __builtin_nontemporal_store(f32x4{v[i], v[i + 1], v[i + 2], v[i + 3]}, reinterpret_cast<f32x4*>(p + i));
+      __builtin_nontemporal_store(u32x4{__float_as_uint(v[i]), __float_as_uint(v[i + 1]),
+                                        __float_as_uint(v[i + 2]), __float_as_uint(v[i + 3])},
+                                  reinterpret_cast<u32x4_any*>(p + i));
   }
 }
 
@@ -620,6 +643,7 @@ __global__ __launch_bounds__(64 * WN * WM, 2) void product_kernel(TileArgs p) {
   const int c8 = lane % C8;
   const int64_t col = c0 + static_cast<int64_t>(wn) * OUT + c8 * 8;  // the lane's, every time
   const bool live = col < p.cols;
+  const int last = p.cols - col < 8 ? static_cast<int>(p.cols - col) - 1 : 7;
   const int chunk = GLU ? (c8 >> 1) * 8 + (c8 & 1) * 2 : c8 * 2;
   const bool odd = C >= 32 && !GLU && (lane & 8);  // these read the second chunk first: no bank twice
   float bias[2][8] = {};
@@ -628,10 +652,7 @@ __global__ __launch_bounds__(64 * WN * WM, 2) void product_kernel(TileArgs p) {
 #pragma unroll
     for (int h = 0; h < (GLU ? 2 : 1); ++h)
 #pragma unroll
-      for (int e = 0; e < 8; e += 4) {
-        const f32x4 t = *reinterpret_cast<const f32x4*>(from + h * p.cols + e);
-        bias[h][e] = t[0]; bias[h][e + 1] = t[1]; bias[h][e + 2] = t[2]; bias[h][e + 3] = t[3];
-      }
+      for (int e = 0; e < 8; ++e) bias[h][e] = from[h * p.cols + (e < last ? e : last)];
   }
 #pragma unroll
   for (int m1 = 0; m1 < MT; m1 += PM) {
@@ -662,14 +683,14 @@ __global__ __launch_bounds__(64 * WN * WM, 2) void product_kernel(TileArgs p) {
       if constexpr (GLU) get(chunk + 4, u);
       if (p.parts > 1) {
         float* to = p.part + part * p.part_stride + (MODE == kDw ? expert * p.high + r : r) * width + col;
-        put8<STREAM>(to, v);
-        if constexpr (GLU) put8<STREAM>(to + p.cols, u);
+        put8<STREAM>(to, v, last);
+        if constexpr (GLU) put8<STREAM>(to + p.cols, u, last);
         continue;
       }
       if constexpr (MODE == kDx) {
-        put8<STREAM>(static_cast<Act*>(p.out) + r * p.cols + col, v);
+        put8<STREAM>(static_cast<Act*>(p.out) + r * p.cols + col, v, last);
       } else if constexpr (MODE == kDw) {
-        put8<STREAM>(static_cast<Act*>(p.out) + (expert * p.high + r) * p.cols + col, v);
+        put8<STREAM>(static_cast<Act*>(p.out) + (expert * p.high + r) * p.cols + col, v, last);
       } else {
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
@@ -677,8 +698,8 @@ __global__ __launch_bounds__(64 * WN * WM, 2) void product_kernel(TileArgs p) {
           if constexpr (GLU) u[e] += bias[1][e];
         }
         if (p.pre) {
-          put8<STREAM>(static_cast<Act*>(p.pre) + r * width + col, v);
-          if constexpr (GLU) put8<STREAM>(static_cast<Act*>(p.pre) + r * width + p.cols + col, u);
+          put8<STREAM>(static_cast<Act*>(p.pre) + r * width + col, v, last);
+          if constexpr (GLU) put8<STREAM>(static_cast<Act*>(p.pre) + r * width + p.cols + col, u, last);
         }
         if (is_silu(p.act)) {
 #pragma unroll
@@ -694,18 +715,22 @@ __global__ __launch_bounds__(64 * WN * WM, 2) void product_kernel(TileArgs p) {
         if (p.residual) {
           if (p.out_f32) {
             Run8<float> t;
-            t.load(static_cast<const float*>(p.residual) + r * p.cols + col);
+            const float* res = static_cast<const float*>(p.residual) + r * p.cols + col;
+            if (last < 7) t.load_elems(res, last);
+            else t.load(res);
 #pragma unroll
             for (int e = 0; e < 8; ++e) v[e] += t.get(e);
           } else {
             Run8<bf16_t> t;
-            t.load(static_cast<const bf16_t*>(p.residual) + r * p.cols + col);
+            const bf16_t* res = static_cast<const bf16_t*>(p.residual) + r * p.cols + col;
+            if (last < 7) t.load_elems(res, last);
+            else t.load(res);
 #pragma unroll
             for (int e = 0; e < 8; ++e) v[e] += t.get(e);
           }
         }
-        if (p.out_f32) put8<STREAM>(static_cast<float*>(p.out) + r * p.cols + col, v);
-        else put8<STREAM>(static_cast<bf16_t*>(p.out) + r * p.cols + col, v);
+        if (p.out_f32) put8<STREAM>(static_cast<float*>(p.out) + r * p.cols + col, v, last);
+        else put8<STREAM>(static_cast<bf16_t*>(p.out) + r * p.cols + col, v, last);
       }
     }
   }
@@ -727,50 +752,47 @@ struct JoinArgs {
 };
 
 __global__ __launch_bounds__(256) void join_kernel(JoinArgs p) {
-  const int64_t quads = p.cols / 4, at = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+  const int64_t quads = (p.cols + 3) / 4, at = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
   const int64_t row = at / quads, c = (at - row * quads) * 4;
   if (row >= p.rows || (p.limit && row >= *p.limit)) return;
   const bool glu = is_gated(p.act);
   const int64_t width = glu ? 2 * p.cols : p.cols;
+  const int last = p.cols - c < 4 ? static_cast<int>(p.cols - c) - 1 : 3;
   f32x4 v = {}, u = {};
   for (int q = 0; q < p.parts; ++q) {
     const float* from = p.part + q * p.part_stride + row * width + c;
-    v += *reinterpret_cast<const f32x4*>(from);
-    if (glu) u += *reinterpret_cast<const f32x4*>(from + p.cols);
+    v += load4(from, last);
+    if (glu) u += load4(from + p.cols, last);
   }
   if (p.bias) {
-    int64_t e = 0;
-    if (p.offsets)
-      for (int lo = 0, hi = p.experts; lo < hi;) {  // the last expert that starts at or before the row
-        const int mid = (lo + hi) / 2;
-        if (p.offsets[mid + 1] <= row) lo = mid + 1;
+    int e = 0;
+    if (p.offsets) {
+      for (int hi = p.experts - 1; e < hi;) {  // the first expert that ends past the row
+        const int mid = (e + hi) / 2;
+        if (p.offsets[mid + 1] <= row) e = mid + 1;
         else hi = mid;
-        e = lo;
       }
-    if (e >= p.experts && p.experts > 0) e = p.experts - 1;
+    }
     const float* bias = p.bias + e * width + c;
-    v += *reinterpret_cast<const f32x4*>(bias);
-    if (glu) u += *reinterpret_cast<const f32x4*>(bias + p.cols);
+    v += load4(bias, last);
+    if (glu) u += load4(bias + p.cols, last);
   }
   if (p.pre) {
     Act* pre = static_cast<Act*>(p.pre) + row * width + c;
-    store4(pre, v);
-    if (glu) store4(pre + p.cols, u);
+    store4(pre, v, last);
+    if (glu) store4(pre + p.cols, u, last);
   }
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
     if (glu) v[j] = bend(p.act, v[j]) * u[j];
     else if (p.act != kNoAct) v[j] = bend(p.act, v[j]);
   }
-  if (p.residual) {
-    float r[4];
-    if (p.out_f32) load4(static_cast<const float*>(p.residual) + row * p.cols + c, r);
-    else load4(static_cast<const bf16_t*>(p.residual) + row * p.cols + c, r);
-#pragma unroll
-    for (int j = 0; j < 4; ++j) v[j] += r[j];
-  }
-  if (p.out_f32) store4(static_cast<float*>(p.out) + row * p.cols + c, v);
-  else store4(static_cast<bf16_t*>(p.out) + row * p.cols + c, v);
+  const int64_t to = row * p.cols + c;
+  if (p.residual)
+    v += p.out_f32 ? load4(static_cast<const float*>(p.residual) + to, last)
+                   : load4(static_cast<const bf16_t*>(p.residual) + to, last);
+  if (p.out_f32) store4(static_cast<float*>(p.out) + to, v, last);
+  else store4(static_cast<bf16_t*>(p.out) + to, v, last);
 }
 
 // ---- few rows: the weights' stream ----
@@ -877,26 +899,23 @@ __global__ __launch_bounds__(64 * kStreamWaves) void stream_kernel(TileArgs p) {
       }
       const int64_t r = m0 + m * 16 + i, c = c0 + quad * 4;
       if (r >= range.to || c >= p.cols) continue;
+      const int last = p.cols - c < 4 ? static_cast<int>(p.cols - c) - 1 : 3;
 #pragma unroll
       for (int h = 0; h < H; ++h) {
-        if (p.bias)
-          v[h] += *reinterpret_cast<const f32x4*>(p.bias + (static_cast<int64_t>(expert) * H + h) * p.cols + c);
-        if (p.pre) store4(static_cast<Act*>(p.pre) + (r * H + h) * p.cols + c, v[h]);
+        if (p.bias) v[h] += load4(p.bias + (static_cast<int64_t>(expert) * H + h) * p.cols + c, last);
+        if (p.pre) store4(static_cast<Act*>(p.pre) + (r * H + h) * p.cols + c, v[h], last);
       }
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         if (GLU) v[0][j] = bend(p.act, v[0][j]) * v[H - 1][j];
         else if (p.act != kNoAct) v[0][j] = bend(p.act, v[0][j]);
       }
-      if (p.residual) {
-        float e[4];
-        if (p.out_f32) load4(static_cast<const float*>(p.residual) + r * p.cols + c, e);
-        else load4(static_cast<const bf16_t*>(p.residual) + r * p.cols + c, e);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) v[0][j] += e[j];
-      }
-      if (p.out_f32) store4(static_cast<float*>(p.out) + r * p.cols + c, v[0]);
-      else store4(static_cast<bf16_t*>(p.out) + r * p.cols + c, v[0]);
+      const int64_t to = r * p.cols + c;
+      if (p.residual)
+        v[0] += p.out_f32 ? load4(static_cast<const float*>(p.residual) + to, last)
+                          : load4(static_cast<const bf16_t*>(p.residual) + to, last);
+      if (p.out_f32) store4(static_cast<float*>(p.out) + to, v[0], last);
+      else store4(static_cast<bf16_t*>(p.out) + to, v[0], last);
     }
     __syncthreads();
   }
@@ -915,6 +934,7 @@ struct BendArgs {
   const int32_t* offsets;
   int experts, act, tile;
   int64_t rows, n, max_tiles;
+  int64_t ld;               // of dpre's rows: nw, up to the next multiple of 8; zeros past nw
 };
 
 // Rows of a tile: few where that leaves the CUs without work.
@@ -933,18 +953,24 @@ __global__ __launch_bounds__(256) void bend_kernel(BendArgs p) {
   const int64_t c = static_cast<int64_t>(blockIdx.y) * 512 + lane * 8;
   const bool live = c < p.n, glu = is_gated(p.act);
   const int64_t width = glu ? 2 * p.n : p.n;
+  const int last = p.n - c < 8 ? static_cast<int>(p.n - c) - 1 : 7;
+  const int pad = static_cast<int>(p.ld - width);
   float sum[16] = {};
   if (live) {
     for (int64_t r = m0 + wave; r < m_end; r += 4) {
+      auto load = [&](auto& run, const auto* from) __attribute__((always_inline)) {
+        if (last < 7) run.load_elems(from, last);
+        else run.load(from);
+      };
       Run8<D> d;
-      d.load(static_cast<const D*>(p.dout) + r * p.n + c);
+      load(d, static_cast<const D*>(p.dout) + r * p.n + c);
       float g[8], h[8] = {};
 #pragma unroll
       for (int e = 0; e < 8; ++e) g[e] = d.get(e);
       if (p.act != kNoAct) {
         Run8<Act> v, u;
-        v.load(static_cast<const Act*>(p.pre) + r * width + c);
-        if (glu) u.load(static_cast<const Act*>(p.pre) + r * width + p.n + c);
+        load(v, static_cast<const Act*>(p.pre) + r * width + c);
+        if (glu) load(u, static_cast<const Act*>(p.pre) + r * width + p.n + c);
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
           float slope;
@@ -957,9 +983,11 @@ __global__ __launch_bounds__(256) void bend_kernel(BendArgs p) {
         }
       }
       if (p.dpre) {
-        Act* to = static_cast<Act*>(p.dpre) + r * width + c;
-        store8(to, g);
-        if (glu) store8(to + p.n, h);
+        Act* to = static_cast<Act*>(p.dpre) + r * p.ld + c;
+        store8(to, g, last);
+        if (glu) store8(to + p.n, h, last);
+        if (c + 8 >= p.n)  // the row's end, which the products read
+          for (int e = 0; e < pad; ++e) store_act(static_cast<Act*>(p.dpre), r * p.ld + width + e, 0.0f);
       }
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
@@ -1131,8 +1159,10 @@ void launch_join(const TileArgs& t, int64_t rows, bool of_rows, int act, hipStre
   j.residual = t.residual;
   j.out = t.out;
   j.pre = t.pre;
-  join_kernel<<<static_cast<unsigned>(div_up64(rows * (t.cols / 4), 256)), 256, 0, stream>>>(j);
+  join_kernel<<<static_cast<unsigned>(div_up64(rows * div_up64(t.cols, 4), 256)), 256, 0, stream>>>(j);
 }
+
+int64_t ld_dpre(const ProductArgs& a) { return div_up64(a.nw(), 8) * 8; }
 
 struct BwdLayout {
   Plan dx, dw;
@@ -1143,9 +1173,10 @@ struct BwdLayout {
 
 BwdLayout bwd_layout(const ProductArgs& a) {
   BwdLayout l = {};
-  const bool copy = a.act != kNoAct || a.out_dtype != a.dtype;
+  // dout serves as dpre unless its rows are not whole runs of 16 bytes
+  const bool copy = a.act != kNoAct || a.out_dtype != a.dtype || a.n % 8;
   l.bend = copy || a.dbias;
-  l.dpre = copy ? up16(a.rows * a.nw() * kSize) : 0;
+  l.dpre = copy ? up16(a.rows * ld_dpre(a) * kSize) : 0;
   l.tiles = most_tiles(a.rows, a.experts, bend_rows(a.rows, a.n));
   l.bias = a.dbias ? up16(l.tiles * a.nw() * 4) : 0;
   if (a.dx) {
@@ -1231,6 +1262,7 @@ hipError_t SSM_TYPED(launch_product_bwd)(const ProductArgs& a, hipStream_t strea
     b.tile = bend_rows(a.rows, a.n);
     b.rows = a.rows;
     b.n = a.n;
+    b.ld = ld_dpre(a);
     b.max_tiles = l.tiles;
     const dim3 grid(static_cast<unsigned>(l.tiles), static_cast<unsigned>(div_up64(a.n, 512)));
     if (a.out_dtype == 0) bend_kernel<float><<<grid, 256, 0, stream>>>(b);
@@ -1249,7 +1281,7 @@ hipError_t SSM_TYPED(launch_product_bwd)(const ProductArgs& a, hipStream_t strea
   t.out_f32 = a.dtype == 0;
   t.part = reinterpret_cast<float*>(work + l.dpre + l.bias);
   t.b = dpre;
-  t.ldb = nw;
+  t.ldb = ld_dpre(a);
   t.cols = a.k;
   if (a.dx) {
     t.a = a.w;

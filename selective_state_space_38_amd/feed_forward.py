@@ -260,8 +260,8 @@ def _product_args(x, w, offsets, token, activation, out_code):
         if nw % 2:
             raise ValueError("a gated activation needs two halves of w's rows")
         n = nw // 2
-    if code < 0 or n % 8 or k % 8:
-        raise ValueError("the sizes of w must be multiples of 8 (its halves' with a gated activation)")
+    if k % 8:
+        raise ValueError("the columns of x and w must be a multiple of 8")
     return (_lib.ProductDims(rows, n, k, x_rows, ld, experts, act, code,
                              code if out_code is None else out_code), dev, lead, nw)
 
@@ -336,8 +336,7 @@ def linear_fwd(x, w, bias=None, activation=None, residual=None, return_pre=False
     [..., n] (n / 2 with those two) of out's type, which is out_dtype, residual's
     or else x's.  out may be residual itself, to add in place.  Returns out, or
     (out, pre) with return_pre: the values before the activation, in x's type, as
-    linear_bwd takes them.  n (its half) and k must be multiples of 8, the tensors
-    16-byte aligned.
+    linear_bwd takes them.  k must be a multiple of 8, the tensors 16-byte aligned.
     """
     return _linear_fwd(x, w, None, None, bias, activation, residual, return_pre, out_dtype, out)
 

@@ -144,7 +144,7 @@ def _bwd(d, **kw):
 
 
 @pytest.mark.parametrize("kw", [
-    dict(rows=0), dict(n=0), dict(k=0), dict(n=12), dict(k=20), dict(x_rows=0), dict(ld_x=16),
+    dict(rows=0), dict(n=0), dict(k=0), dict(k=20), dict(x_rows=0), dict(ld_x=16),
     dict(ld_x=28), dict(experts=-1), dict(experts=1025), dict(activation=5), dict(activation=-1),
     dict(rows=(1 << 30) + 8, x_rows=(1 << 30) + 8), dict(n=(1 << 20) + 8),
     dict(k=(1 << 20) + 8, ld_x=(1 << 20) + 8), dict(rows=1 << 30, x_rows=1 << 30, n=1 << 20),
