@@ -802,10 +802,16 @@ __global__ __launch_bounds__(256) void join_kernel(JoinArgs p) {
 // matrix (of a gated one 16 of either half), its waves the blocks of 128 bytes in
 // turn; the activations come from the L2.  The waves' sums meet in LDS and are added
 // in wave order.  A matrix with more than 16 MT rows is read again for the next ones.
+//
+// Two workgroups a CU, 16 waves, keep the reads in flight: with three registers more
+// than 128 a lane it is one, and 8 tokens' rows of 4 of 64 experts (2560 -> 2 x 1280 gated,
+// bfloat16, 340 MB of weights) take 70 us, not 52 (6.5 TB/s); with fewer blocks in flight
+// for three workgroups 71.  One dense matrix of 26 MB and 8 rows is over before the reads
+// reach their rate: 10.8 us.
 constexpr int kStreamWaves = 8;
 
 template <int MT, bool GLU>
-__global__ __launch_bounds__(64 * kStreamWaves) void stream_kernel(TileArgs p) {
+__global__ __launch_bounds__(64 * kStreamWaves, 4) void stream_kernel(TileArgs p) {
   constexpr int H = GLU ? 2 : 1;
   __shared__ f32x4 s_sum[kStreamWaves][H * MT][64];
   const int lane = threadIdx.x & 63, i = lane & 15, quad = lane >> 4;
@@ -865,7 +871,7 @@ __global__ __launch_bounds__(64 * kStreamWaves) void stream_kernel(TileArgs p) {
       xrow[m] = static_cast<const char*>(p.b) + (in[m] ? t : 0) * p.ldb * kSize;
     }
     f32x4 acc[H][MT] = {};
-    constexpr int U = MT * H == 1 ? 4 : MT * H == 2 ? 3 : 2;  // blocks in flight
+    constexpr int U = MT * H == 1 ? 4 : 2;  // blocks in flight
     for (int g0 = w; g0 < groups; g0 += U * W) {
       i32x8 a[U][H], b[U][MT];
 #pragma unroll
@@ -1057,7 +1063,6 @@ struct Plan {
 constexpr int kStreamRows = 32;
 constexpr int64_t kCus = 256;
 
-
 // Most tiles of `side` rows that `rows` rows of the experts make: each expert's last
 // may be filled in part.
 int64_t most_tiles(int64_t rows, int experts, int64_t side) {
@@ -1066,37 +1071,59 @@ int64_t most_tiles(int64_t rows, int experts, int64_t side) {
   return rows / side + some;
 }
 
-// height: rows of D on the average matrix; cols: of D with both halves
+constexpr int kMostParts = 32;
+
+// What one block of the summed axis takes on a CU that has `n` tiles of this shape to
+// do, in us, for all of them: the figures of products that fill 1 to 40 tiles a CU, within
+// a tenth of the measured times with 2 blocks (float32) or 5 (bfloat16) added a tile for
+// its start and its epilogue.  A float32 tile keeps the matrix units busy by itself, so
+// that tiles of one CU add up; a bfloat16 tile waits for its loads, and a second of
+// 128 x 128 or three more of 64 x 64 run meanwhile.
+double block_us(int shape, int64_t n) {
+  const double d = static_cast<double>(n);
+  if (kSize == 4) return d * (shape == kTile256 ? 7.9 : shape == kTile128 ? 2.06 : 0.56);
+  if (shape == kTile256) return 1.4 * d;
+  if (shape == kTile128) return 0.9 * (n / 2) + 0.75 * (n % 2);
+  return 0.72 * (n / 4) + (n % 4 ? 0.45 + 0.05 * (n % 4) : 0.0);
+}
+
+// The tile and the parts of the summed axis of the least cost: what the fullest CU has
+// to do, and for parts the join, 4 us and its traffic at 5 TB/s.  The largest tile moves
+// the least memory, but 276 of them keep 256 CUs for two rounds, the second nearly
+// empty: float32, 11686 rows x 1344 x 2960 takes 1469 us by 256 x 256 tiles and 768 by
+// 128 x 128 ones, bfloat16 4096 x 5120 x 2560 126 and 116; bfloat16 2048 x 5120 x 2560 60
+// (160 tiles, one round) and 79.  Few tiles with a long sum are split: bfloat16, the rows'
+// gradient of 1024 x 5120 x 2560 takes 64 us by 160 tiles of 128 x 128, 48 by two parts of each.
+// kStreamRows rows or fewer of a matrix: every wave would read the weights for a tile of
+// rows that are mostly padding, and the stream kernel reads them straight into registers.
 Plan plan_tiles(const ProductArgs& a, int mode) {
   Plan q = {kTile64, 1};
   const int64_t nw = a.nw(), matrices = a.experts ? a.experts : 1;
   const int64_t cols = mode == kDx || mode == kDw ? a.k : nw;
   const int64_t high = mode == kDw ? nw : div_up64(a.rows, matrices);
   const int64_t depth = mode == kDw ? div_up64(a.rows, matrices) : mode == kDx ? nw : a.k;
-  auto tiles = [&](int64_t side) { return matrices * div_up64(high, side) * div_up64(cols, side); };
-  if (tiles(256) >= 150 && high > 128) q.shape = kTile256;
-  else if (tiles(128) >= 256 && high > 64) q.shape = kTile128;
-  if ((mode == kFwd || mode == kGlu) && high <= kStreamRows) q.shape = kStream;
-  const int shape = forced("SSM_FORCE_PRODUCT_SHAPE"), parts = forced("SSM_FORCE_PRODUCT_PARTS");
-  if (shape >= kTile64 && shape <= kTile256) q.shape = shape;
-  if (shape == kStream && (mode == kFwd || mode == kGlu)) q.shape = kStream;
-  if (q.shape == kStream) return q;
   const int64_t blocks = div_up64(depth, kBlock);
-  if (q.shape == kTile64) {
-    // a block takes 0.42 us, of float32 on every CU, of bfloat16 three workgroups a CU
-    // at a time; the join 4 us and its traffic, written and read at 2.5 TB/s
-    const int64_t slots = kSize == 4 ? kCus : 3 * kCus;
-    const double values = static_cast<double>(matrices) * high * cols;
-    double best = 0.0;
-    for (int t = 1; t <= 8 && t <= blocks; ++t) {
-      const double rounds = static_cast<double>(div_up64(tiles(64) * t, slots));
-      const double us = 0.42 * rounds * div_up64(blocks, t) + (t > 1 ? 4.0 + 8e-6 / 2.5 * values * t : 0.0);
-      if (t == 1 || us < best) {
+  const double values = static_cast<double>(matrices) * high * cols;
+  if ((mode == kFwd || mode == kGlu) && high <= kStreamRows) q.shape = kStream;
+  double best = 0.0;
+  const int sides[] = {64, 128, 256}, shapes[] = {kTile64, kTile128, kTile256};
+  for (int s = 0; s < 3 && q.shape != kStream; ++s) {
+    const int64_t all = matrices * div_up64(high, sides[s]) * div_up64(cols, sides[s]);
+    for (int t = 1; t <= (shapes[s] == kTile256 ? 1 : kMostParts) && t <= blocks; ++t) {
+      const int64_t mine = div_up64(all * t, kCus);
+      double us = (div_up64(blocks, t) + (kSize == 4 ? 2 : 5)) * block_us(shapes[s], mine);
+      if (t > 1) us += 4.0 + 8e-6 / 5.0 * values * t;
+      if ((s == 0 && t == 1) || us < best) {
         best = us;
+        q.shape = shapes[s];
         q.parts = t;
       }
     }
   }
+  const int shape = forced("SSM_FORCE_PRODUCT_SHAPE"), parts = forced("SSM_FORCE_PRODUCT_PARTS");
+  if (shape >= kTile64 && shape <= kTile256) q = {shape, 1};
+  if (shape == kStream && (mode == kFwd || mode == kGlu)) q = {kStream, 1};
+  if (q.shape == kStream) return q;
   if (parts > 0) q.parts = parts;
   if (q.parts > blocks) q.parts = static_cast<int>(blocks);
   // with each = ceil(blocks / parts), drop the parts without a block
