@@ -15,6 +15,13 @@ namespace ssm {
 // rounding decides it; equal ones go to the lowest index, which is the lowest
 // lane's.  A NaN counts as the lowest finite logit there, and -inf is never
 // chosen.
+//
+// The instructions of the choice bound it, k rounds of a maximum over V values and L
+// lanes: of bfloat16 logits over one word of value and number, 8.8 us for 32768 tokens of 128
+// experts, k 8 (12.2 by a maximum, a search for its lane and that lane's number, as float32
+// logits need; the logits' 8 MB and what is written take 2.4).  16 lanes a token keep the
+// maximum in one row of the wave, without LDS; from 257 experts on a lane would hold
+// more than 16, and the whole wave takes a token.
 
 template <typename T, int L, int V>
 struct Scores {
@@ -26,6 +33,19 @@ struct Scores {
     v = row16_max(v);
     if constexpr (L == 64) {
       v = fmaxf(fmaxf(read_lane(v, 0), read_lane(v, 16)), fmaxf(read_lane(v, 32), read_lane(v, 48)));
+    }
+    return v;
+  }
+  __device__ __forceinline__ static uint32_t all_max(uint32_t v) {
+    auto higher = [](uint32_t a, uint32_t b) { return a > b ? a : b; };
+    auto turned = [&](auto by) { return __float_as_uint(row_ror<by.value>(__uint_as_float(v))); };
+    v = higher(v, turned(std::integral_constant<int, 8>{}));
+    v = higher(v, turned(std::integral_constant<int, 4>{}));
+    v = higher(v, turned(std::integral_constant<int, 2>{}));
+    v = higher(v, turned(std::integral_constant<int, 1>{}));
+    if constexpr (L == 64) {
+      auto row = [&](int at) { return static_cast<uint32_t>(__builtin_amdgcn_readlane(v, at)); };
+      v = higher(higher(row(0), row(16)), higher(row(32), row(48)));
     }
     return v;
   }
@@ -91,6 +111,15 @@ struct Scores {
 constexpr int kRouteThreads = 256;
 constexpr float kLowest = -3.402823466e38f;  // the lowest finite value
 
+// A bfloat16's place among them as the upper half of a word: -inf the lowest, then a NaN
+// with the lowest finite value, both zeros one.
+constexpr uint32_t kLowestOrder = 0x00800000u;
+__device__ __forceinline__ uint32_t order_of(float x) {
+  const uint32_t b = __float_as_uint(x + 0.0f);  // -0 + 0 = 0
+  const uint32_t o = (b >> 31 ? ~b : b | 0x80000000u) & 0xffff0000u;
+  return x != x ? kLowestOrder : o;
+}
+
 template <typename T, int L, int V>
 __global__ __launch_bounds__(kRouteThreads) void route_fwd_kernel(RouteArgs p) {
   using S = Scores<T, L, V>;
@@ -110,39 +139,61 @@ __global__ __launch_bounds__(kRouteThreads) void route_fwd_kernel(RouteArgs p) {
       for (int v = 0; v < V; ++v)
         if (r.first + v < E) total[v] += r.s[v];
     }
-    float key[V];
-#pragma unroll
-    for (int v = 0; v < V; ++v) key[v] = r.x[v] != r.x[v] ? kLowest : r.x[v];
-    float mine = 0.0f, sum = 0.0f, top = 0.0f;  // choice `at`'s weight; lanes 0 .. K - 1
+    float mine = -__builtin_inff();  // choice `at`'s logit; lanes 0 .. K - 1
     int chosen = -1;
-    for (int j = 0; j < K; ++j) {
-      float m = key[0];
+    if constexpr (sizeof(T) == 2) {
+      // one word a logit: the value's order in the upper half, ahead of it the lower index
+      uint32_t key[V], won = 0;
 #pragma unroll
-      for (int v = 1; v < V; ++v) m = fmaxf(m, key[v]);
-      m = S::all_max(m);
-      if (m == -__builtin_inff()) break;
-      int v_of = -1;  // the lane's first of them
+      for (int v = 0; v < V; ++v) key[v] = order_of(r.x[v]) | (0xffffu - (r.first + v));
+      for (int j = 0; j < K; ++j) {
+        uint32_t m = key[0];
 #pragma unroll
-      for (int v = V - 1; v >= 0; --v) v_of = key[v] == m ? v : v_of;
-      const uint64_t hit = __ballot(v_of >= 0) >> (group * L) & (L == 64 ? ~0ull : 0xffffull);
-      const int who = __builtin_ctzll(hit);
-      const int e = __shfl(r.first + v_of, group * L + who);
-      if (at == who) {
+        for (int v = 1; v < V; ++v) m = key[v] > m ? key[v] : m;
+        m = S::all_max(m);
+        if (m < kLowestOrder) break;
 #pragma unroll
-        for (int v = 0; v < V; ++v) key[v] = v == v_of ? -__builtin_inff() : key[v];
+        for (int v = 0; v < V; ++v) key[v] = key[v] == m ? 0 : key[v];
+        if (at == j) won = m;
       }
-      // its logit is m but for a NaN that counts as the lowest
-      float x = m;
-      if (m == kLowest) {
-        float own = 0.0f;
-#pragma unroll
-        for (int v = 0; v < V; ++v) own = v == v_of ? r.x[v] : own;
-        x = __shfl(own, group * L + who);
+      if (won) {
+        chosen = 0xffff - (won & 0xffff);
+        mine = __uint_as_float((won >> 31 ? won ^ 0x80000000u : ~won) & 0xffff0000u);
+        if ((won & 0xffff0000u) == kLowestOrder)  // or a NaN
+          mine = to_f32(static_cast<const T*>(p.logits)[(live ? t : p.tokens - 1) * E + chosen]);
       }
-      if (j == 0) top = x;
-      const float s = p.renormalize ? S::share(x, top, p.sigmoid) : r.score_of(x, p.sigmoid);
-      sum += s;
-      if (at == j) mine = s, chosen = e;
+    } else {
+      float key[V];
+#pragma unroll
+      for (int v = 0; v < V; ++v) key[v] = r.x[v] != r.x[v] ? kLowest : r.x[v];
+      for (int j = 0; j < K; ++j) {
+        float m = key[0];
+#pragma unroll
+        for (int v = 1; v < V; ++v) m = fmaxf(m, key[v]);
+        m = S::all_max(m);
+        if (m == -__builtin_inff()) break;
+        int v_of = -1;  // the lane's first of them
+#pragma unroll
+        for (int v = V - 1; v >= 0; --v) v_of = key[v] == m ? v : v_of;
+        const uint64_t hit = __ballot(v_of >= 0) >> (group * L) & (L == 64 ? ~0ull : 0xffffull);
+        const int who = __builtin_ctzll(hit);
+        const int e = __shfl(r.first + v_of, group * L + who);
+        if (at == who) {
+#pragma unroll
+          for (int v = 0; v < V; ++v) key[v] = v == v_of ? -__builtin_inff() : key[v];
+        }
+        if (at == j) mine = m, chosen = e;
+      }
+      if (chosen >= 0 && mine == kLowest)  // or a NaN
+        mine = to_f32(static_cast<const T*>(p.logits)[(live ? t : p.tokens - 1) * E + chosen]);
+    }
+    const float top = __shfl(mine, group * L);
+    float sum = 1.0f;
+    if (p.renormalize) {
+      mine = chosen >= 0 ? S::share(mine, top, p.sigmoid) : 0.0f;
+      sum = S::all_sum(mine);
+    } else {
+      mine = r.score_of(mine, p.sigmoid);
     }
     if (live && at < K) {
       p.index[t * K + at] = chosen;
@@ -298,14 +349,18 @@ hipError_t launch_route_bwd(const RouteArgs& a, hipStream_t stream) {
 // ---- order ----
 //
 // A stable counting sort.  A workgroup takes kSortEntries pairs (token, choice) in
-// their order, each of its waves a run of them, 64 at a time: the lanes that hold
-// the same expert find each other by one ballot per bit of its number, so a
-// pair's rank among its wave's is a population count, and the wave's counters
-// stand in LDS.  Nothing is added by atomics: the order is the pairs' own.  With
-// more than one workgroup a first launch counts; each workgroup of the second
-// adds up the counts of those before it.
+// their order, 64 a wave: the lanes that hold the same expert find each other by one
+// ballot per bit of its number, so a pair's rank among its wave's is a population
+// count, and the waves' counters stand in LDS.  The order is the pairs' own, whatever
+// runs first.  With more than one workgroup a first launch counts; each workgroup of the
+// last adds up the counts of those before it, or a launch between does.
+//
+// 262144 pairs of 128 experts: 2.9 + 8.5 us, a chain of short steps over 1 MB read and
+// 2 MB written; with four runs a wave, a quarter of the workgroups, 3.6 + 10.8.  16384 of 64
+// experts: 2.6 + 5.8 us, 3.2 + 8.3 with four.
 
 constexpr int kSortWaves = 16;
+constexpr int64_t kSortEntries = 64 * kSortWaves;
 
 __device__ __forceinline__ uint64_t same_lanes(int e, int bits) {
   uint64_t same = ~0ull;
@@ -322,34 +377,35 @@ __device__ __forceinline__ int bin_of(int e, int experts) {
   return static_cast<unsigned>(e) < static_cast<unsigned>(experts) ? e : experts;
 }
 
-// counts[workgroup][E + 1]
-template <int ROUNDS>
+// Counts of a workgroup's pairs, 16 bits each, an even number of them.
+__host__ __device__ __forceinline__ int count_words(int experts) { return (experts + 1) / 2; }
+
+// counts[workgroup][2 count_words]
 __global__ __launch_bounds__(64 * kSortWaves) void sort_count_kernel(SortArgs p, int64_t entries) {
-  extern __shared__ int s_count[];  // [E + 1]
-  const int bins = p.experts + 1;
-  for (int e = threadIdx.x; e < bins; e += blockDim.x) s_count[e] = 0;
+  extern __shared__ int s_count[];  // [2 words]
+  const int words = count_words(p.experts);
+  for (int e = threadIdx.x; e < 2 * words; e += blockDim.x) s_count[e] = 0;
   __syncthreads();
-  const int64_t from = static_cast<int64_t>(blockIdx.x) * (64 * kSortWaves * ROUNDS);
-#pragma unroll
-  for (int r = 0; r < ROUNDS; ++r) {
-    const int64_t i = from + r * (64 * kSortWaves) + threadIdx.x;
-    if (i < entries) atomicAdd(&s_count[bin_of(p.index[i], p.experts)], 1);  // whole numbers: any order
+  const int64_t i = static_cast<int64_t>(blockIdx.x) * kSortEntries + threadIdx.x;
+  if (i < entries) {
+    const int bin = bin_of(p.index[i], p.experts);
+    if (bin < p.experts) atomicAdd(&s_count[bin], 1);  // whole numbers: any order
   }
   __syncthreads();
-  int* to = static_cast<int*>(p.work) + static_cast<int64_t>(blockIdx.x) * bins;
-  for (int e = threadIdx.x; e < bins; e += blockDim.x) to[e] = s_count[e];
+  uint32_t* to = static_cast<uint32_t*>(p.work) + static_cast<int64_t>(blockIdx.x) * words;
+  for (int w = threadIdx.x; w < words; w += blockDim.x) to[w] = s_count[2 * w] | s_count[2 * w + 1] << 16;
 }
 
-// Column e of counts[groups][E + 1] becomes its exclusive sums, their total in row
-// `groups`: one workgroup a column.
-__global__ __launch_bounds__(256) void sort_scan_kernel(int* counts, int groups, int bins) {
+// Exclusive sums over the workgroups of an expert's counts, their total behind: one workgroup
+// an expert.
+__global__ __launch_bounds__(256) void sort_scan_kernel(const uint16_t* counts, int stride, int groups,
+                                                        int experts, int* sums) {
   __shared__ int s_sum[4];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  int* column = counts + blockIdx.x;
   int carry = 0;
   for (int g0 = 0; g0 < groups; g0 += 256) {
     const int g = g0 + threadIdx.x;
-    const int c = g < groups ? column[static_cast<int64_t>(g) * bins] : 0;
+    const int c = g < groups ? counts[static_cast<int64_t>(g) * stride + blockIdx.x] : 0;
     int run = c;
 #pragma unroll
     for (int d = 1; d < 64; d *= 2) {
@@ -364,43 +420,29 @@ __global__ __launch_bounds__(256) void sort_scan_kernel(int* counts, int groups,
       if (w < wave) ahead += s_sum[w];
       carry += s_sum[w];
     }
-    if (g < groups) column[static_cast<int64_t>(g) * bins] = ahead + run - c;
+    if (g < groups) sums[static_cast<int64_t>(g) * experts + blockIdx.x] = ahead + run - c;
   }
-  if (threadIdx.x == 0) column[static_cast<int64_t>(groups) * bins] = carry;
+  if (threadIdx.x == 0) sums[static_cast<int64_t>(groups) * experts + blockIdx.x] = carry;
 }
 
-// scanned: counts hold exclusive sums; otherwise, with several workgroups, counts.
-template <int ROUNDS>
+// scanned: the exclusive sums, or null.
 __global__ __launch_bounds__(64 * kSortWaves) void sort_place_kernel(SortArgs p, int64_t entries,
-                                                                     int bits, bool scanned) {
-  extern __shared__ int lds[];  // first place [E + 1], totals [E + 1], sums [waves], counters [waves][E + 1]
+                                                                     int bits, const int* scanned) {
+  extern __shared__ int lds[];  // first place, totals [E + 1], sums [2 waves], counters [waves][E + 1]
   const int bins = p.experts + 1;
   int* place = lds;
   int* s_total = place + bins;
   int* sums = s_total + bins;
-  uint16_t* counters = reinterpret_cast<uint16_t*>(sums + kSortWaves);
+  uint16_t* counters = reinterpret_cast<uint16_t*>(sums + 2 * kSortWaves);
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   for (int e = threadIdx.x; e < kSortWaves * bins; e += blockDim.x) counters[e] = 0;
-  const int64_t from = static_cast<int64_t>(blockIdx.x) * (64 * kSortWaves * ROUNDS) +
-                       wave * (64 * ROUNDS) + lane;
-  int bin[ROUNDS], rank[ROUNDS];
-#pragma unroll
-  for (int r = 0; r < ROUNDS; ++r)
-    bin[r] = from + 64 * r < entries ? bin_of(p.index[from + 64 * r], p.experts) : -1;
+  const int64_t i = static_cast<int64_t>(blockIdx.x) * kSortEntries + threadIdx.x;
+  const int bin = i < entries ? bin_of(p.index[i], p.experts) : -1;
   __syncthreads();
-  volatile uint16_t* own = counters + wave * bins;
-#pragma unroll
-  for (int r = 0; r < ROUNDS; ++r) {
-    const uint64_t same = same_lanes(bin[r], bits) & __ballot(bin[r] >= 0);
-    const int before = __popcll(same & ((1ull << lane) - 1));
-    int base = 0;
-    if (bin[r] >= 0) base = own[bin[r]];
-    rank[r] = base + before;
-    __builtin_amdgcn_wave_barrier();
-    // the lowest of the lanes writes for all: one writer per counter
-    if (bin[r] >= 0 && before == 0) own[bin[r]] = static_cast<uint16_t>(base + __popcll(same));
-    __builtin_amdgcn_wave_barrier();
-  }
+  const uint64_t same = same_lanes(bin, bits) & __ballot(bin >= 0);
+  const int rank = __popcll(same & ((1ull << lane) - 1));
+  // the lowest of the lanes writes for all: one writer per counter
+  if (bin >= 0 && rank == 0) counters[wave * bins + bin] = static_cast<uint16_t>(__popcll(same));
   __syncthreads();
   // the waves' counters become places within the workgroup's run of a bin
   const int e = threadIdx.x;
@@ -415,57 +457,61 @@ __global__ __launch_bounds__(64 * kSortWaves) void sort_place_kernel(SortArgs p,
     if (b == e) total = sum;
   }
   const int groups = static_cast<int>(gridDim.x), mine = static_cast<int>(blockIdx.x);
-  const int* counts = static_cast<const int*>(p.work);
-  int missing = 0;  // pairs without an expert in the workgroups before (thread 0)
   if (groups > 1 && scanned) {
-    if (e < bins) {
-      earlier = counts[static_cast<int64_t>(mine) * bins + e];
-      total = counts[static_cast<int64_t>(groups) * bins + e];
+    if (e < p.experts) {
+      earlier = scanned[static_cast<int64_t>(mine) * p.experts + e];
+      total = scanned[static_cast<int64_t>(groups) * p.experts + e];
     }
-    if (e == 0) missing = counts[static_cast<int64_t>(mine) * bins + p.experts];
   } else if (groups > 1) {
-    // 1024 / span threads a bin, each every so many-th workgroup's count
+    // 1024 / span threads a word of two counts, each every so many-th workgroup's
+    const uint32_t* counts = static_cast<const uint32_t*>(p.work);
+    const int words = count_words(p.experts);
     int span = 64;
-    while (span < bins) span *= 2;
-    if (span > blockDim.x) span = blockDim.x;  // the last bin (none) is thread 0's below
-    const int stride = blockDim.x / span, bin0 = e % span;
-    int all = 0, ahead = 0;
+    while (span < words) span *= 2;
+    const int stride = blockDim.x / span, word = e % span;
+    int all[2] = {}, ahead[2] = {};
 #pragma unroll 8
     for (int g = e / span; g < groups; g += stride) {
-      const int c = bin0 < bins ? counts[g * bins + bin0] : 0;
-      ahead += g < mine ? c : 0;
-      all += c;
+      const uint32_t c = word < words ? counts[g * words + word] : 0;
+      const int c0 = c & 0xffff, c1 = c >> 16;
+      all[0] += c0;
+      all[1] += c1;
+      ahead[0] += g < mine ? c0 : 0;
+      ahead[1] += g < mine ? c1 : 0;
     }
     for (int b = e; b < bins; b += blockDim.x) place[b] = s_total[b] = 0;
     __syncthreads();
-    if (bin0 < bins) {
-      atomicAdd(&s_total[bin0], all);  // whole numbers: any order
-      atomicAdd(&place[bin0], ahead);
+    if (word < words) {
+      for (int h = 0; h < 2; ++h) {  // behind an odd number of experts: none, to the last bin
+        atomicAdd(&s_total[2 * word + h], all[h]);  // whole numbers: any order
+        atomicAdd(&place[2 * word + h], ahead[h]);
+      }
     }
     __syncthreads();
-    total = e < bins ? s_total[e] : 0;
-    earlier = e < bins ? place[e] : 0;
-    if (e == 0) {
-      missing = p.experts < span ? place[p.experts] : 0;
-      for (int g = 0; g < mine && p.experts >= span; ++g) missing += counts[g * bins + p.experts];
-    }
+    total = e < p.experts ? s_total[e] : 0;
+    earlier = e < p.experts ? place[e] : 0;
     __syncthreads();
   }
   // exclusive sums over the experts (the bin of pairs without one starts where the
   // experts' end)
   const int own_total = e < p.experts ? total : 0;
-  int run = own_total;
+  int run = own_total, before = earlier;
 #pragma unroll
   for (int d = 1; d < 64; d *= 2) {
     const int up = __shfl_up(run, d);
     if (lane >= d) run += up;
+    before += __shfl_xor(before, d);
   }
-  if (lane == 63) sums[wave] = run;
+  if (lane == 63) {
+    sums[wave] = run;
+    sums[kSortWaves + wave] = before;
+  }
   __syncthreads();
-  int ahead = 0, all = 0;
+  int ahead = 0, all = 0, taken = 0;  // by the workgroups before
   for (int w = 0; w < kSortWaves; ++w) {
     if (w < wave) ahead += sums[w];
     all += sums[w];
+    taken += sums[kSortWaves + w];
   }
   const int start = ahead + run - own_total;
   if (e < p.experts) {
@@ -473,52 +519,51 @@ __global__ __launch_bounds__(64 * kSortWaves) void sort_place_kernel(SortArgs p,
     if (mine == 0) p.offsets[e] = start;
   }
   if (e == 0) {
-    place[p.experts] = all + missing;
+    place[p.experts] = all + mine * static_cast<int>(kSortEntries) - taken;
     if (mine == 0) p.offsets[p.experts] = all;
   }
   __syncthreads();
-#pragma unroll
-  for (int r = 0; r < ROUNDS; ++r) {
-    if (bin[r] < 0) continue;
-    const int64_t i = from + 64 * r;
-    const int at = place[bin[r]] + counters[wave * bins + bin[r]] + rank[r];
-    const bool in = bin[r] < p.experts;
-    p.slot[i] = in ? at : -1;
-    p.token[at] = in ? static_cast<int32_t>(i / p.topk) : -1;
-  }
+  if (bin < 0) return;
+  const int at = place[bin] + counters[wave * bins + bin] + rank;
+  const bool in = bin < p.experts;
+  p.slot[i] = in ? at : -1;
+  p.token[at] = in ? static_cast<int32_t>(i / p.topk) : -1;
 }
 
-// Pairs a workgroup takes: 64 per wave up to that many in all, then 256.
-static int sort_rounds(int64_t entries) { return entries <= 64 * kSortWaves ? 1 : 4; }
-// More workgroups than this have their counts summed by a launch of its own.
-constexpr int64_t kSortDirect = 64;
+// More words of counts than these are summed by a launch of its own: of 16384 (262144 pairs
+// of 128 experts) the sums take every workgroup 2.1 us, the launch 3 and a gap.
+constexpr int64_t kSortDirect = 20000;
+
+static int64_t sort_sums_at(int64_t groups, int experts) {
+  return (groups * count_words(experts) * 4 + 15) / 16 * 16;
+}
+
+static bool sort_scans(int64_t groups, int experts) {
+  return groups > 1 && groups * count_words(experts) > kSortDirect;
+}
 
 int64_t sort_work(int64_t entries, int experts) {
-  const int64_t groups = div_up64(entries, 64 * kSortWaves * sort_rounds(entries));
-  return groups > 1 ? (groups + 1) * (experts + 1) * 4 : 0;
-}
-
-template <int ROUNDS>
-static void launch_sort_rounds(const SortArgs& a, int64_t entries, hipStream_t stream) {
-  const int64_t groups = div_up64(entries, 64 * kSortWaves * ROUNDS);
-  const unsigned grid = static_cast<unsigned>(groups);
-  const int bins = a.experts + 1;
-  int bits = 1;
-  while (a.experts >> bits) ++bits;
-  if (groups > 1)
-    sort_count_kernel<ROUNDS><<<grid, 64 * kSortWaves, bins * 4, stream>>>(a, entries);
-  if (groups > kSortDirect)
-    sort_scan_kernel<<<bins, 256, 0, stream>>>(static_cast<int*>(a.work), static_cast<int>(groups),
-                                               bins);
-  sort_place_kernel<ROUNDS>
-      <<<grid, 64 * kSortWaves, (2 * bins + kSortWaves) * 4 + kSortWaves * bins * 2, stream>>>(
-          a, entries, bits, groups > kSortDirect);
+  const int64_t groups = div_up64(entries, kSortEntries);
+  if (groups <= 1) return 0;
+  return sort_sums_at(groups, experts) +
+         (sort_scans(groups, experts) ? (groups + 1) * experts * 4 : 0);
 }
 
 hipError_t launch_sort(const SortArgs& a, hipStream_t stream) {
-  const int64_t entries = a.tokens * a.topk;
-  if (sort_rounds(entries) == 1) launch_sort_rounds<1>(a, entries, stream);
-  else launch_sort_rounds<4>(a, entries, stream);
+  const int64_t entries = a.tokens * a.topk, groups = div_up64(entries, kSortEntries);
+  const unsigned grid = static_cast<unsigned>(groups);
+  const int words = count_words(a.experts), bins = a.experts + 1;
+  int* sums = nullptr;
+  int bits = 1;
+  while (a.experts >> bits) ++bits;
+  if (groups > 1) sort_count_kernel<<<grid, 64 * kSortWaves, words * 8, stream>>>(a, entries);
+  if (sort_scans(groups, a.experts)) {
+    sums = reinterpret_cast<int*>(static_cast<char*>(a.work) + sort_sums_at(groups, a.experts));
+    sort_scan_kernel<<<a.experts, 256, 0, stream>>>(static_cast<const uint16_t*>(a.work), 2 * words,
+                                                    static_cast<int>(groups), a.experts, sums);
+  }
+  sort_place_kernel<<<grid, 64 * kSortWaves, (2 * bins + 2 * kSortWaves) * 4 + kSortWaves * bins * 2,
+                      stream>>>(a, entries, bits, sums);
   return hipGetLastError();
 }
 

@@ -141,6 +141,28 @@ def test_values_that_are_not_finite():
             g[0], expert_route_bwd(clean, other[0], torch.ones_like(weight), score=score)[0])
 
 
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("experts", [7, 128, 200, 1000])
+def test_choice_over_every_bit_pattern(experts, dtype):
+    # both zeros are equal, a NaN of either sign is the lowest finite value, -inf is not chosen
+    from selective_state_space_38_amd import expert_route_fwd
+    tokens, k = 700, 6
+    bits = np.random.default_rng(experts).integers(0, 1 << 16, (tokens, experts)).astype(np.uint32)
+    few = np.array([0x0000, 0x8000, 0x7f80, 0xff80, 0x7fc0, 0xffc0, 0x7f81, 0xff7f, 0x7f7f, 0x0001,
+                    0x8001], np.uint32)
+    bits[::2] = few[np.random.default_rng(1).integers(0, len(few), (tokens // 2, experts))]
+    values = (bits << 16).view(np.float32)
+    logits = torch.from_numpy(values).cuda().to(dtype)
+    low = float(torch.finfo(dtype).min)
+    want = ref(logits)
+    want = np.where(np.isnan(want), low, want)
+    index, weight = expert_route_fwd(logits, k)
+    order = np.argsort(-want, axis=1, kind="stable")[:, :k]
+    none = np.take_along_axis(want, order, 1) == -np.inf
+    np.testing.assert_array_equal(index.cpu().numpy(), np.where(none, -1, order))
+    assert (ref(weight)[none] == 0).all()
+
+
 def test_far_logits_keep_their_shares():
     # sigmoids that all but vanish: the chosen ones' shares are still those of exp(l)
     from selective_state_space_38_amd import expert_route_bwd, expert_route_fwd
