@@ -372,8 +372,8 @@ __device__ __forceinline__ void place_of(int64_t t, int64_t tiles_m, int64_t til
 // Consecutive workgroups go to the 8 XCDs in turn: each XCD gets a range of the
 // `tiles` tiles of its own, so that the tiles it has in flight share their operands in
 // its L2.  -1: none left.
-__device__ __forceinline__ int64_t tile_number(int64_t tiles) {
-  const int64_t bid = blockIdx.x, xcd = bid % 8, each = tiles / 8, more = tiles % 8;
+__device__ __forceinline__ int64_t tile_number(int64_t tiles, int64_t bid) {
+  const int64_t xcd = bid % 8, each = tiles / 8, more = tiles % 8;
   if (bid / 8 >= each + (xcd < more ? 1 : 0)) return -1;
   return xcd * each + (xcd < more ? xcd : more) + bid / 8;
 }
@@ -384,8 +384,8 @@ __device__ __forceinline__ int64_t tile_number(int64_t tiles) {
 __host__ __device__ __forceinline__ int64_t expert_grid(int64_t each, int64_t experts) {
   return each < 16 ? each * experts : (each + 7) / 8 * 8 * experts;
 }
-__device__ __forceinline__ bool expert_tile(int64_t each, int64_t experts, int* expert, int64_t* t) {
-  const int64_t bid = blockIdx.x;
+__device__ __forceinline__ bool expert_tile(int64_t each, int64_t experts, int64_t bid, int* expert,
+                                            int64_t* t) {
   if (each < 16) {
     *expert = static_cast<int>(bid / each);
     *t = bid - *expert * each;
@@ -453,16 +453,14 @@ __device__ __forceinline__ void put8(T* p, const float (&v)[8], int last = 7) {
   }
 }
 
+// Tile number `bid`, part `part` of it.  The LDS objects are separate, so that reads of one
+// are known not to wait for loads into another.
 template <int MODE, int BN, int BM, int WN, int WM>
-__global__ __launch_bounds__(64 * WN * WM, 2) void product_kernel(TileArgs p) {
+__device__ __forceinline__ void product_tile(const TileArgs& p, int64_t bid, int part, uint8_t* s_a0,
+                                             uint8_t* s_a1, uint8_t* s_b0, uint8_t* s_b1) {
   constexpr int WAVES = WN * WM, NT = BN / WN / 16, MT = BM / WM / 16;
   constexpr bool GLU = MODE == kGlu, A_COL = MODE == kDx || MODE == kDw, B_COL = MODE == kDw;
   constexpr bool STREAM = BM == 256;
-  // separate objects, so that reads of one are known not to wait for loads into another
-  __shared__ __align__(1024) uint8_t s_a0[BN * kBlockBytes];
-  __shared__ __align__(1024) uint8_t s_a1[BN * kBlockBytes];
-  __shared__ __align__(1024) uint8_t s_b0[BM * kBlockBytes];
-  __shared__ __align__(1024) uint8_t s_b1[BM * kBlockBytes];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wn = wave % WN, wm = wave / WN;
@@ -476,14 +474,14 @@ __global__ __launch_bounds__(64 * WN * WM, 2) void product_kernel(TileArgs p) {
   if constexpr (MODE == kDw) {
     const int64_t tiles_m = (p.high + BM - 1) / BM, each = tiles_m * tiles_n;
     int64_t t;
-    if (!expert_tile(each, p.offsets ? p.experts : 1, &expert, &t)) return;
+    if (!expert_tile(each, p.offsets ? p.experts : 1, bid, &expert, &t)) return;
     place_of(t, tiles_m, tiles_n, &tm, &tn);
     range = rows_of(p.offsets, expert, p.rows);
     m0 = tm * BM;
     m_end = p.high;
   } else {
     const Tiles tiles = {p.offsets, p.experts, p.rows, BM};
-    const int64_t total = tiles.total(), t = tile_number(total * tiles_n);
+    const int64_t total = tiles.total(), t = tile_number(total * tiles_n, bid);
     if (t < 0) return;
     place_of(t, total, tiles_n, &tm, &tn);
     int at;
@@ -494,10 +492,10 @@ __global__ __launch_bounds__(64 * WN * WM, 2) void product_kernel(TileArgs p) {
   }
   const int64_t c0 = tn * kCols;
 
-  // with the summed axis split over gridDim.y workgroups: blocks first .. first + groups - 1
+  // with the summed axis split over p.parts workgroups: blocks first .. first + groups - 1
   const int64_t depth = MODE == kDw ? range.to - range.from : p.depth;
-  const int all = static_cast<int>((depth + kBlock - 1) / kBlock), part = blockIdx.y;
-  const int each = (all + gridDim.y - 1) / gridDim.y, first = part * each;
+  const int all = static_cast<int>((depth + kBlock - 1) / kBlock);
+  const int each = (all + p.parts - 1) / p.parts, first = part * each;
   const int groups = all - first < each ? (all - first > 0 ? all - first : 0) : each;
 
   const Act* a = static_cast<const Act*>(p.a) + (MODE == kDw ? 0 : expert * p.stride_a);
@@ -735,6 +733,34 @@ __global__ __launch_bounds__(64 * WN * WM, 2) void product_kernel(TileArgs p) {
     }
   }
 }
+
+#define SSM_PRODUCT_LDS(SIDE)                                \
+  __shared__ __align__(1024) uint8_t s_a0[SIDE * kBlockBytes]; \
+  __shared__ __align__(1024) uint8_t s_a1[SIDE * kBlockBytes]; \
+  __shared__ __align__(1024) uint8_t s_b0[SIDE * kBlockBytes]; \
+  __shared__ __align__(1024) uint8_t s_b1[SIDE * kBlockBytes]
+
+template <int MODE, int SIDE, int WN, int WM>
+__global__ __launch_bounds__(64 * WN * WM, 2) void product_kernel(TileArgs p) {
+  SSM_PRODUCT_LDS(SIDE);
+  product_tile<MODE, SIDE, SIDE, WN, WM>(p, blockIdx.x, blockIdx.y, s_a0, s_a1, s_b0, s_b1);
+}
+
+// Both products of the gradient by one launch: first the tiles of dw, `each` workgroups (a
+// multiple of the XCDs) for every part, then those of dx, which fill the CUs that the last of
+// the others leave free.
+template <int SIDE, int WN, int WM>
+__global__ __launch_bounds__(64 * WN * WM, 2) void pair_kernel(TileArgs w, TileArgs x, int64_t each) {
+  SSM_PRODUCT_LDS(SIDE);
+  const int64_t bid = blockIdx.x, behind = bid - each * w.parts;
+  if (behind < 0) {
+    const int part = static_cast<int>(bid / each);
+    product_tile<kDw, SIDE, SIDE, WN, WM>(w, bid - part * each, part, s_a0, s_a1, s_b0, s_b1);
+  } else {
+    product_tile<kDx, SIDE, SIDE, WN, WM>(x, behind, 0, s_a0, s_a1, s_b0, s_b1);
+  }
+}
+#undef SSM_PRODUCT_LDS
 
 // Joins the parts of a product whose summed axis was split, in order, four columns a
 // thread.  limit: the last expert's end, past which rows stay as they are (nullable).
@@ -1058,7 +1084,14 @@ enum Shape : int { kStream = 0, kTile64 = 1, kTile128 = 2, kTile256 = 3 };
 
 struct Plan {
   int shape, parts;
+  double us;  // the estimate that they were chosen by
 };
+
+// Parts of `blocks` blocks, each ceil(blocks / parts) of them, without those that get none.
+int whole_parts(int64_t blocks, int parts) {
+  if (parts > blocks) parts = static_cast<int>(blocks);
+  return parts <= 1 ? 1 : static_cast<int>(div_up64(blocks, div_up64(blocks, parts)));
+}
 
 constexpr int kStreamRows = 32;
 constexpr int64_t kCus = 256;
@@ -1096,38 +1129,65 @@ double block_us(int shape, int64_t n) {
 // gradient of 1024 x 5120 x 2560 takes 64 us by 160 tiles of 128 x 128, 48 by two parts of each.
 // kStreamRows rows or fewer of a matrix: every wave would read the weights for a tile of
 // rows that are mostly padding, and the stream kernel reads them straight into registers.
+struct Sizes {  // of a product in tiles
+  int64_t high, cols, blocks, matrices;
+  int64_t tiles(int64_t side) const { return matrices * div_up64(high, side) * div_up64(cols, side); }
+  double join_us(int parts) const {
+    return parts > 1 ? 4.0 + 8e-6 / 5.0 * static_cast<double>(matrices) * high * cols * parts : 0.0;
+  }
+};
+Sizes sizes_of(const ProductArgs& a, int mode) {
+  const int64_t nw = a.nw(), matrices = a.experts ? a.experts : 1, mean = div_up64(a.rows, matrices);
+  if (mode == kDw) return {nw, a.k, div_up64(mean, kBlock), matrices};
+  return {mean, mode == kDx ? a.k : nw, div_up64(mode == kDx ? nw : a.k, kBlock), matrices};
+}
+constexpr int kSides[] = {0, 64, 128, 256};
+constexpr int kExtra = kSize == 4 ? 2 : 5;  // blocks a tile, its start and its epilogue
+
 Plan plan_tiles(const ProductArgs& a, int mode) {
-  Plan q = {kTile64, 1};
-  const int64_t nw = a.nw(), matrices = a.experts ? a.experts : 1;
-  const int64_t cols = mode == kDx || mode == kDw ? a.k : nw;
-  const int64_t high = mode == kDw ? nw : div_up64(a.rows, matrices);
-  const int64_t depth = mode == kDw ? div_up64(a.rows, matrices) : mode == kDx ? nw : a.k;
-  const int64_t blocks = div_up64(depth, kBlock);
-  const double values = static_cast<double>(matrices) * high * cols;
-  if ((mode == kFwd || mode == kGlu) && high <= kStreamRows) q.shape = kStream;
-  double best = 0.0;
-  const int sides[] = {64, 128, 256}, shapes[] = {kTile64, kTile128, kTile256};
-  for (int s = 0; s < 3 && q.shape != kStream; ++s) {
-    const int64_t all = matrices * div_up64(high, sides[s]) * div_up64(cols, sides[s]);
-    for (int t = 1; t <= (shapes[s] == kTile256 ? 1 : kMostParts) && t <= blocks; ++t) {
-      const int64_t mine = div_up64(all * t, kCus);
-      double us = (div_up64(blocks, t) + (kSize == 4 ? 2 : 5)) * block_us(shapes[s], mine);
-      if (t > 1) us += 4.0 + 8e-6 / 5.0 * values * t;
-      if ((s == 0 && t == 1) || us < best) {
-        best = us;
-        q.shape = shapes[s];
-        q.parts = t;
-      }
+  const Sizes z = sizes_of(a, mode);
+  Plan q = {kTile64, 1, 0.0};
+  if ((mode == kFwd || mode == kGlu) && z.high <= kStreamRows) q.shape = kStream;
+  for (int s = kTile64; s <= kTile256 && q.shape != kStream; ++s) {
+    const int64_t all = z.tiles(kSides[s]);
+    for (int t = 1; t <= (s == kTile256 ? 1 : kMostParts) && t <= z.blocks; ++t) {
+      const double us =
+          (div_up64(z.blocks, t) + kExtra) * block_us(s, div_up64(all * t, kCus)) + z.join_us(t);
+      if ((s == kTile64 && t == 1) || us < q.us) q = {s, t, us};
     }
   }
   const int shape = forced("SSM_FORCE_PRODUCT_SHAPE"), parts = forced("SSM_FORCE_PRODUCT_PARTS");
-  if (shape >= kTile64 && shape <= kTile256) q = {shape, 1};
-  if (shape == kStream && (mode == kFwd || mode == kGlu)) q = {kStream, 1};
+  if (shape >= kTile64 && shape <= kTile256) q = {shape, 1, 0.0};
+  if (shape == kStream && (mode == kFwd || mode == kGlu)) q = {kStream, 1, 0.0};
   if (q.shape == kStream) return q;
   if (parts > 0) q.parts = parts;
-  if (q.parts > blocks) q.parts = static_cast<int>(blocks);
-  // with each = ceil(blocks / parts), drop the parts without a block
-  q.parts = static_cast<int>(div_up64(blocks, div_up64(blocks, q.parts)));
+  q.parts = whole_parts(z.blocks, q.parts);
+  return q;
+}
+
+// Both products of the gradient by one launch, dw in parts: of shape kStream if two are better.
+// What the CUs have to do is shared evenly but for half a tile at the end: bfloat16, 16384 x
+// 5120 x 2560 in 200 tiles of 256 blocks and 640 of 80, 753 us against 808 by two launches,
+// 2048 x 1536 x 768 27 against 42, 32768 x 5120 x 2560, whole rounds by themselves, 1520 either
+// way.  float32 tiles of 64 x 64 leave little over (2047 x 768 x 1536 112 and 111).
+Plan plan_pair(const ProductArgs& a, const Plan& dx, const Plan& dw) {
+  const Sizes x = sizes_of(a, kDx), w = sizes_of(a, kDw);
+  Plan q = {kStream, 1, dx.us + dw.us + 2.0};
+  const int pair = forced("SSM_FORCE_PRODUCT_PAIR"), shape = forced("SSM_FORCE_PRODUCT_SHAPE"),
+            parts = forced("SSM_FORCE_PRODUCT_PARTS");
+  if (pair == 0 || (pair < 0 && (shape >= 0 || dx.parts > 1))) return q;
+  for (int s = kTile64; s <= kTile256; ++s) {
+    if (shape >= 0 && s != shape) continue;
+    const int full = s == kTile64 ? 4 : s == kTile128 ? 2 : 1;  // tiles that a CU works on at once
+    for (int t = 1; t <= kMostParts && t <= w.blocks; ++t) {
+      const double one = block_us(s, 1), own = div_up64(w.blocks, t) + kExtra, other = x.blocks + kExtra;
+      const double shared = (w.tiles(kSides[s]) * t * own + x.tiles(kSides[s]) * other) / kCus *
+                                block_us(s, full) / full + 0.5 * other * one;
+      const double us = (shared > own * one ? shared : own * one) + w.join_us(t);
+      if (us < q.us || (pair > 0 && q.shape == kStream)) q = {s, t, us};
+    }
+  }
+  if (q.shape != kStream) q.parts = whole_parts(w.blocks, parts > 0 ? parts : q.parts);
   return q;
 }
 
@@ -1142,15 +1202,19 @@ int64_t parts_bytes(const ProductArgs& a, int mode, const Plan& q) {
   return up16(q.parts * values * 4);
 }
 
+// Workgroups for the tiles of one part.
+template <int MODE, int SIDE>
+int64_t grid_of(const TileArgs& t) {
+  const int experts = t.offsets ? t.experts : 0;
+  const int64_t tiles_n = div_up64(t.cols, MODE == kGlu ? SIDE / 2 : SIDE);
+  if (MODE == kDw) return expert_grid(div_up64(t.high, SIDE) * tiles_n, experts ? experts : 1);
+  return most_tiles(t.rows, experts, SIDE) * tiles_n;
+}
+
 template <int MODE, int SIDE, int WN, int WM>
 void launch_side(const TileArgs& t, hipStream_t stream) {
-  constexpr int kCols = MODE == kGlu ? SIDE / 2 : SIDE;
-  const int experts = t.offsets ? t.experts : 0;
-  const int64_t tiles_n = div_up64(t.cols, kCols);
-  const int64_t tiles = MODE == kDw ? expert_grid(div_up64(t.high, SIDE) * tiles_n, experts ? experts : 1)
-                                    : most_tiles(t.rows, experts, SIDE) * tiles_n;
-  const dim3 grid(static_cast<unsigned>(tiles), t.parts);
-  product_kernel<MODE, SIDE, SIDE, WN, WM><<<grid, 64 * WN * WM, 0, stream>>>(t);
+  const dim3 grid(static_cast<unsigned>(grid_of<MODE, SIDE>(t)), t.parts);
+  product_kernel<MODE, SIDE, WN, WM><<<grid, 64 * WN * WM, 0, stream>>>(t);
 }
 
 template <int MODE>
@@ -1158,6 +1222,19 @@ void launch_tiles(const TileArgs& t, int shape, hipStream_t stream) {
   if (shape == kTile256) launch_side<MODE, 256, 2, 4>(t, stream);
   else if (shape == kTile128) launch_side<MODE, 128, 2, 2>(t, stream);
   else launch_side<MODE, 64, 2, 2>(t, stream);
+}
+
+template <int SIDE, int WN, int WM>
+void launch_pair_side(const TileArgs& w, const TileArgs& x, hipStream_t stream) {
+  const int64_t each = div_up64(grid_of<kDw, SIDE>(w), 8) * 8;
+  const unsigned grid = static_cast<unsigned>(each * w.parts + grid_of<kDx, SIDE>(x));
+  pair_kernel<SIDE, WN, WM><<<grid, 64 * WN * WM, 0, stream>>>(w, x, each);
+}
+
+void launch_pair(const TileArgs& w, const TileArgs& x, int shape, hipStream_t stream) {
+  if (shape == kTile256) launch_pair_side<256, 2, 4>(w, x, stream);
+  else if (shape == kTile128) launch_pair_side<128, 2, 2>(w, x, stream);
+  else launch_pair_side<64, 2, 2>(w, x, stream);
 }
 
 template <int MT>
@@ -1193,6 +1270,7 @@ int64_t ld_dpre(const ProductArgs& a) { return div_up64(a.nw(), 8) * 8; }
 
 struct BwdLayout {
   Plan dx, dw;
+  bool pair;                // both products by one launch
   bool bend;                // a pass over dout is needed
   int64_t dpre, bias, parts, total;  // bytes
   int64_t tiles;
@@ -1212,6 +1290,15 @@ BwdLayout bwd_layout(const ProductArgs& a) {
   }
   if (a.dw) {
     l.dw = plan_tiles(a, kDw);
+    if (a.dx) {
+      const Plan both = plan_pair(a, l.dx, l.dw);
+      l.pair = both.shape != kStream;
+      if (l.pair) {
+        l.dx = {both.shape, 1, 0.0};
+        l.dw = both;
+        l.parts = 0;
+      }
+    }
     const int64_t b = parts_bytes(a, kDw, l.dw);
     l.parts = b > l.parts ? b : l.parts;  // one after the other: the same place
   }
@@ -1300,39 +1387,40 @@ hipError_t SSM_TYPED(launch_product_bwd)(const ProductArgs& a, hipStream_t strea
     }
     if (l.dpre) dpre = work;
   }
-  TileArgs t = {};
-  t.rows = a.rows;
-  t.x_rows = a.x_rows;
-  t.offsets = offsets;
-  t.experts = a.experts;
-  t.out_f32 = a.dtype == 0;
-  t.part = reinterpret_cast<float*>(work + l.dpre + l.bias);
-  t.b = dpre;
-  t.ldb = ld_dpre(a);
-  t.cols = a.k;
-  if (a.dx) {
-    t.a = a.w;
-    t.lda = a.k;
-    t.stride_a = nw * a.k;
-    t.depth = nw;
-    t.out = a.dx;
-    t.parts = l.dx.parts;
-    t.part_stride = a.rows * a.k;
-    launch_tiles<kDx>(t, l.dx.shape, stream);
-    if (t.parts > 1) launch_join(t, a.rows, true, kNoAct, stream);
+  const int64_t matrices = a.experts ? a.experts : 1;
+  TileArgs x = {};
+  x.rows = a.rows;
+  x.x_rows = a.x_rows;
+  x.offsets = offsets;
+  x.experts = a.experts;
+  x.out_f32 = a.dtype == 0;
+  x.part = reinterpret_cast<float*>(work + l.dpre + l.bias);
+  x.b = dpre;
+  x.ldb = ld_dpre(a);
+  x.cols = a.k;
+  TileArgs w = x;
+  x.a = a.w;
+  x.lda = a.k;
+  x.stride_a = nw * a.k;
+  x.depth = nw;
+  x.out = a.dx;
+  x.parts = l.dx.parts;
+  x.part_stride = a.rows * a.k;
+  w.a = a.x;
+  w.lda = a.ld_x;
+  w.high = nw;
+  w.token = a.token;
+  w.out = a.dw;
+  w.parts = l.dw.parts;
+  w.part_stride = matrices * nw * a.k;
+  if (l.pair) launch_pair(w, x, l.dw.shape, stream);
+  if (a.dx && !l.pair) {
+    launch_tiles<kDx>(x, l.dx.shape, stream);
+    if (x.parts > 1) launch_join(x, a.rows, true, kNoAct, stream);
   }
   if (a.dw) {
-    const int64_t matrices = a.experts ? a.experts : 1;
-    t.a = a.x;
-    t.lda = a.ld_x;
-    t.stride_a = 0;
-    t.high = nw;
-    t.token = a.token;
-    t.out = a.dw;
-    t.parts = l.dw.parts;
-    t.part_stride = matrices * nw * a.k;
-    launch_tiles<kDw>(t, l.dw.shape, stream);
-    if (t.parts > 1) launch_join(t, matrices * nw, false, kNoAct, stream);
+    if (!l.pair) launch_tiles<kDw>(w, l.dw.shape, stream);
+    if (w.parts > 1) launch_join(w, matrices * nw, false, kNoAct, stream);
   }
   return hipGetLastError();
 }

@@ -67,15 +67,32 @@ def check_fwd(x, w, bias, act, res, got, pre, offsets=None):
     assert (diff <= bound).all(), f"{(diff / bound).max():.3g} of the bound"
 
 
-@pytest.fixture(params=["planned", "rows", "64", "64 in 3", "128", "128 in 2", "256"])
-def shape(request, monkeypatch):
+def choose(name, monkeypatch):
     """Which kernel runs: what the sizes choose, or one of them."""
-    if request.param != "planned":
-        name, _, parts = request.param.partition(" in ")
-        monkeypatch.setenv("SSM_FORCE_PRODUCT_SHAPE", str(["rows", "64", "128", "256"].index(name)))
-        if parts:
-            monkeypatch.setenv("SSM_FORCE_PRODUCT_PARTS", parts)
-    return request.param
+    if name == "planned":
+        return name
+    both, _, rest = name.rpartition("both ")
+    side, _, parts = rest.partition(" in ")
+    monkeypatch.setenv("SSM_FORCE_PRODUCT_SHAPE", str(["rows", "64", "128", "256"].index(side)))
+    monkeypatch.setenv("SSM_FORCE_PRODUCT_PAIR", str(int("both" in name)))
+    if parts:
+        monkeypatch.setenv("SSM_FORCE_PRODUCT_PARTS", parts)
+    return name
+
+
+SHAPES = ["planned", "rows", "64", "64 in 3", "128", "128 in 2", "256"]
+
+
+@pytest.fixture(params=SHAPES)
+def shape(request, monkeypatch):
+    return choose(request.param, monkeypatch)
+
+
+# ("both": dx and dw by one launch, dw in so many parts)
+@pytest.fixture(params=[s for s in SHAPES if s != "rows"] +
+                ["both 64", "both 64 in 3", "both 128", "both 128 in 2", "both 256"])
+def back_shape(request, monkeypatch):
+    return choose(request.param, monkeypatch)
 
 
 @pytest.mark.parametrize("dtype", DTYPES)
@@ -203,9 +220,7 @@ def check_bwd(got, dout, x, w, pre, act, dtype, exact_dpre, bias, offsets=None):
 @pytest.mark.parametrize("dtype", DTYPES)
 @pytest.mark.parametrize("act", ACTS)
 @pytest.mark.parametrize("rows,n,k", DENSE)
-def test_linear_gradient(rows, n, k, act, dtype, shape):
-    if shape == "rows":
-        pytest.skip("the forward's kernel")
+def test_linear_gradient(rows, n, k, act, dtype, back_shape):
     from selective_state_space_38_amd import linear_bwd
     nw = widths(n, act)
     x, w = rand(rows, k, dtype=dtype), rand(nw, k, dtype=dtype, seed=1)
@@ -218,7 +233,9 @@ def test_linear_gradient(rows, n, k, act, dtype, shape):
     for key, kw in (("dx", dict(need_dw=False)), ("dw", dict(need_dx=False)),
                     ("dbias", dict(need_dx=False, need_dw=False, bias=True))):
         one = linear_bwd(dout, x, w, activation=act, pre=pre, **kw)
-        assert set(one) == {key} and torch.equal(one[key], g[key])
+        assert set(one) == {key}
+        if "both" not in back_shape:  # (the parts of a sum may differ)
+            assert torch.equal(one[key], g[key])
     # the other type's dout
     other = torch.float32 if dtype == torch.bfloat16 else torch.bfloat16
     dout = rand(rows, n, dtype=other, seed=3)
@@ -229,9 +246,7 @@ def test_linear_gradient(rows, n, k, act, dtype, shape):
 @pytest.mark.parametrize("dtype", DTYPES)
 @pytest.mark.parametrize("act", [None, "silu", "geglu"])
 @pytest.mark.parametrize("counts", COUNTS, ids=lambda c: f"{len(c)}x{max(c)}")
-def test_expert_linear_gradient(counts, act, dtype, shape):
-    if shape == "rows":
-        pytest.skip("the forward's kernel")
+def test_expert_linear_gradient(counts, act, dtype, back_shape):
     from selective_state_space_38_amd import expert_linear_bwd
     n, k, rows = (72 if len(counts) % 2 else 75), 136, 50
     nw = widths(n, act)
@@ -262,7 +277,7 @@ def test_expert_linear_gradient(counts, act, dtype, shape):
 
 
 @pytest.mark.parametrize("dtype", DTYPES)
-def test_a_row_that_is_not_finite_stays_its_own(dtype, shape):
+def test_a_row_that_is_not_finite_stays_its_own(dtype, shape, monkeypatch):
     from selective_state_space_38_amd import expert_linear_bwd, expert_linear_fwd
     counts, n, k = [5, 40, 3, 70], 72, 136
     x, offsets, token = experts_of(counts, 118, k, dtype)
@@ -276,7 +291,8 @@ def test_a_row_that_is_not_finite_stays_its_own(dtype, shape):
     rest = [r for r in range(118) if r not in (44, 45)]
     assert got[44].isnan().all() and torch.equal(got[rest], clean[rest])
     if shape == "rows":
-        return
+        monkeypatch.delenv("SSM_FORCE_PRODUCT_SHAPE")
+        monkeypatch.setenv("SSM_FORCE_PRODUCT_PAIR", "1")
     dout = rand(118, n, dtype=dtype, seed=2)
     a = expert_linear_bwd(dout, x, w, offsets, token=token, bias=True)
     b = expert_linear_bwd(dout, bad, w, offsets, token=token, bias=True)
@@ -290,7 +306,7 @@ def test_a_row_that_is_not_finite_stays_its_own(dtype, shape):
     assert torch.equal(a["dbias"][[0, 2, 3]], b["dbias"][[0, 2, 3]]) and b["dbias"][1].isnan().all()
 
 
-def test_offsets_outside_the_rows_stay_inside(shape):
+def test_offsets_outside_the_rows_stay_inside(shape, monkeypatch):
     # what the host cannot check: nothing outside the given arrays is touched
     from selective_state_space_38_amd import expert_linear_bwd, expert_linear_fwd
     n, k, rows = 24, 40, 37
@@ -301,7 +317,8 @@ def test_offsets_outside_the_rows_stay_inside(shape):
         whole = guard.clone()
         expert_linear_fwd(x, w, offsets, out=whole[:rows])
         assert torch.equal(whole[rows:], guard[rows:])
-        if shape != "rows":
+        for both in "01":
+            monkeypatch.setenv("SSM_FORCE_PRODUCT_PAIR", both)
             expert_linear_bwd(whole[:rows], x, w, offsets, bias=True)
     torch.cuda.synchronize()
 
