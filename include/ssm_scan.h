@@ -667,7 +667,7 @@ typedef enum {
 } ssm_score;
 
 /* Sizes of a router.  experts at most 1024; topk at most 16 and at most experts;
- * tokens * topk at most 2^30. */
+ * tokens at most 2^25, tokens * topk at most 2^30. */
 typedef struct {
   int64_t tokens;
   int32_t experts;
@@ -711,8 +711,8 @@ int expert_route_bwd(const void* logits, float scale, const int32_t* index,
 
 /*
  * The order by expert: rows offsets[e] .. offsets[e + 1] - 1 are expert e's, in
- * the order of (token, choice); limits as of route_dims, but topk may exceed
- * experts (a token may name an expert twice).
+ * the order of (token, choice).  experts at most 1024, topk at most 16 (it may exceed
+ * experts: a token may name an expert twice), tokens * topk at most 2^30.
  *   index   : [tokens][topk]; an entry outside 0 .. experts - 1 has no row
  *   offsets : [experts + 1]
  *   token   : [tokens * topk], the token of every row; -1 past offsets[experts]
@@ -726,8 +726,8 @@ int expert_sort(const int32_t* index, int64_t tokens, int32_t topk,
 
 /* Sizes of the way into the order and back: rows of dim values. */
 typedef struct {
-  int64_t tokens;
-  int64_t rows;            /* of xs, y, dy; at most 2^30 */
+  int64_t tokens;          /* at most 2^25 */
+  int64_t rows;            /* of xs, y, dy; at most 2^25 */
   int64_t dim;
   int32_t topk;            /* at most 16 */
   int32_t dtype;           /* ssm_dtype of x, xs, y, dy */
@@ -769,7 +769,8 @@ typedef enum {
   SSM_ACT_GEGLU = 4    /* gelu(first half) * second half */
 } ssm_activation;
 
-/* Sizes of a product: nw = n, or 2 n with a gated activation. */
+/* Sizes of a product: nw = n, or 2 n with a gated activation.  Of its outputs, of
+ * [rows][k] and of [experts][nw][k] at most 2^21 tiles of 256 x 256. */
 typedef struct {
   int64_t rows;
   int64_t n;            /* columns of out */

@@ -42,11 +42,14 @@ int check_pairs(int64_t tokens, int32_t experts, int32_t topk) {
   return tokens > (1LL << 30) / topk ? SSM_EINVAL : SSM_OK;
 }
 
+// 16 or 64 lanes a token, or a row: a launch has fewer than 2^32.
+constexpr int64_t kMostTokens = 1LL << 25;
+
 int check_route(const route_dims* d) {
   if (!d) return SSM_EINVAL;
   if (!valid_dtype(d->dtype)) return SSM_EDTYPE;
   if (d->score != SSM_SOFTMAX && d->score != SSM_SIGMOID) return SSM_EINVAL;
-  if (d->topk > d->experts) return SSM_EINVAL;
+  if (d->topk > d->experts || d->tokens > kMostTokens) return SSM_EINVAL;
   return check_pairs(d->tokens, d->experts, d->topk);
 }
 
@@ -66,7 +69,7 @@ ssm::RouteArgs route_args(const route_dims* d, const void* logits, float scale) 
 int check_order(const order_dims* d) {
   if (!d) return SSM_EINVAL;
   if (!valid_dtype(d->dtype) || !valid_dtype(d->residual_dtype)) return SSM_EDTYPE;
-  if (d->rows <= 0 || d->rows > (1LL << 30) || d->dim <= 0 || d->dim > (1LL << 24)) return SSM_EINVAL;
+  if (d->rows <= 0 || d->rows > kMostTokens || d->tokens > kMostTokens || d->dim <= 0 || d->dim > (1LL << 24)) return SSM_EINVAL;
   return check_pairs(d->tokens, 1, d->topk);
 }
 
@@ -93,11 +96,10 @@ int check_product(const product_dims* d) {
   if (d->rows > (1LL << 30) || d->x_rows > (1LL << 30) || d->n > (1LL << 20) || d->k > (1LL << 20))
     return SSM_EINVAL;
   const int64_t nw = d->activation >= SSM_ACT_SWIGLU ? 2 * d->n : d->n;
-  const int64_t row_tiles = ssm::div_up64(d->rows, 64) + d->experts;
-  const int64_t wide = ssm::div_up64(nw > d->k ? nw : d->k, 32);
-  if (row_tiles * wide > (1LL << 31) - 1) return SSM_EINVAL;
+  const int64_t row_tiles = ssm::div_up64(d->rows, 256) + d->experts;
+  if (row_tiles * ssm::div_up64(nw > d->k ? nw : d->k, 256) > ssm::kMostTiles) return SSM_EINVAL;
   const int64_t matrices = d->experts ? d->experts : 1;
-  if (matrices * ssm::div_up64(nw, 64) * ssm::div_up64(d->k, 64) > (1LL << 31) - 1) return SSM_EINVAL;
+  if (matrices * ssm::div_up64(nw, 256) * ssm::div_up64(d->k, 256) > ssm::kMostTiles) return SSM_EINVAL;
   if (d->rows * ssm::div_up64(nw > d->k ? nw : d->k, 1024) > (1LL << 31) - 1) return SSM_EINVAL;
   if (matrices * nw * ssm::div_up64(d->k, 1024) > (1LL << 31) - 1) return SSM_EINVAL;
   return SSM_OK;

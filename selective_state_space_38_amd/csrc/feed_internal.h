@@ -65,6 +65,10 @@ hipError_t launch_gather(const OrderArgs& a, hipStream_t stream);
 hipError_t launch_combine_fwd(const OrderArgs& a, hipStream_t stream);
 hipError_t launch_combine_bwd(const OrderArgs& a, hipStream_t stream);
 
+// Tiles of a product's launch at most: fewer than 2^32 lanes, an expert's padding and the other
+// product of the gradient included.
+constexpr int64_t kMostTiles = 1 << 21;
+
 // A linear product's sizes and operands.  nw = n, or 2 n of a gated activation.
 struct ProductArgs {
   int dtype, out_dtype, act, experts;  // experts 0: one matrix for all rows

@@ -1150,10 +1150,11 @@ Plan plan_tiles(const ProductArgs& a, int mode) {
   if ((mode == kFwd || mode == kGlu) && z.high <= kStreamRows) q.shape = kStream;
   for (int s = kTile64; s <= kTile256 && q.shape != kStream; ++s) {
     const int64_t all = z.tiles(kSides[s]);
+    if (all > kMostTiles && s != kTile256) continue;
     for (int t = 1; t <= (s == kTile256 ? 1 : kMostParts) && t <= z.blocks; ++t) {
       const double us =
           (div_up64(z.blocks, t) + kExtra) * block_us(s, div_up64(all * t, kCus)) + z.join_us(t);
-      if ((s == kTile64 && t == 1) || us < q.us) q = {s, t, us};
+      if (q.us == 0.0 || us < q.us) q = {s, t, us};
     }
   }
   const int shape = forced("SSM_FORCE_PRODUCT_SHAPE"), parts = forced("SSM_FORCE_PRODUCT_PARTS");
@@ -1178,8 +1179,9 @@ Plan plan_pair(const ProductArgs& a, const Plan& dx, const Plan& dw) {
   if (pair == 0 || (pair < 0 && (shape >= 0 || dx.parts > 1))) return q;
   for (int s = kTile64; s <= kTile256; ++s) {
     if (shape >= 0 && s != shape) continue;
+    if (x.tiles(kSides[s]) > kMostTiles) continue;
     const int full = s == kTile64 ? 4 : s == kTile128 ? 2 : 1;  // tiles that a CU works on at once
-    for (int t = 1; t <= kMostParts && t <= w.blocks; ++t) {
+    for (int t = 1; t <= kMostParts && t <= w.blocks && w.tiles(kSides[s]) * t <= kMostTiles; ++t) {
       const double one = block_us(s, 1), own = div_up64(w.blocks, t) + kExtra, other = x.blocks + kExtra;
       const double shared = (w.tiles(kSides[s]) * t * own + x.tiles(kSides[s]) * other) / kCus *
                                 block_us(s, full) / full + 0.5 * other * one;

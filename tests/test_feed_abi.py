@@ -54,7 +54,7 @@ def _route_bwd(d, **kw):
 @pytest.mark.parametrize("kw", [
     dict(tokens=0), dict(tokens=-1), dict(experts=0), dict(experts=1025), dict(topk=0),
     dict(topk=9), dict(topk=17, experts=64), dict(score=2), dict(score=-1),
-    dict(tokens=1 << 30, topk=2)])
+    dict(tokens=1 << 30, topk=2), dict(tokens=(1 << 25) + 1, topk=1)])
 def test_route_dims(kw):
     d = _route(**kw)
     assert _route_fwd(d) == _route_bwd(d) == SSM_EINVAL
@@ -114,7 +114,8 @@ def test_order_arguments():
 
     for f in (gather, fwd, bwd):
         for kw in (dict(tokens=0), dict(rows=0), dict(dim=0), dict(topk=0), dict(topk=17),
-                   dict(rows=(1 << 30) + 1), dict(dim=(1 << 24) + 1)):
+                   dict(rows=(1 << 30) + 1), dict(rows=(1 << 25) + 1), dict(tokens=(1 << 25) + 1),
+                   dict(dim=(1 << 24) + 1)):
             assert f(_order(**kw)) == SSM_EINVAL, kw
         assert f(_order(dtype=4)) == f(_order(residual_dtype=4)) == SSM_EDTYPE
     d = _order()
@@ -148,6 +149,7 @@ def _bwd(d, **kw):
     dict(ld_x=28), dict(experts=-1), dict(experts=1025), dict(activation=5), dict(activation=-1),
     dict(rows=(1 << 30) + 8, x_rows=(1 << 30) + 8), dict(n=(1 << 20) + 8),
     dict(k=(1 << 20) + 8, ld_x=(1 << 20) + 8), dict(rows=1 << 30, x_rows=1 << 30, n=1 << 20),
+    dict(rows=1 << 30, x_rows=1 << 30), dict(experts=1024, n=1 << 18, k=1 << 18, ld_x=1 << 18),
     dict(x_rows=9)])
 def test_product_dims(kw):
     d = _product(**kw)

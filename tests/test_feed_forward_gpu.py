@@ -105,7 +105,6 @@ def test_layer_of_experts(tokens, dim, hidden, experts, k):
 
 def test_dropped_choices():
     # experts take 20 rows each: what is past that adds nothing and gets no gradient
-    import selective_state_space_38_amd as ssm
     v = layer_of(200, 64, 40, 4)
     got = run(v, 2, capacity=20)
     index = got["index"]
@@ -116,7 +115,6 @@ def test_dropped_choices():
     assert torch.equal(got["out"][gone], v["x"][gone])
     for key in ("dw1", "dw2", "dx", "dwr"):
         assert torch.isfinite(got[key]).all()
-    del ssm
 
 
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
