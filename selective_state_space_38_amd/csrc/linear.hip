@@ -1170,10 +1170,11 @@ Plan plan_tiles(const ProductArgs& a, int mode) {
 // What the CUs have to do is shared evenly but for half a tile at the end: bfloat16, 16384 x
 // 5120 x 2560 in 200 tiles of 256 blocks and 640 of 80, 753 us against 808 by two launches,
 // 2048 x 1536 x 768 27 against 42, 32768 x 5120 x 2560, whole rounds by themselves, 1520 either
-// way.  float32 tiles of 64 x 64 leave little over (2047 x 768 x 1536 112 and 111).
+// way.  A tile of dw that is much longer than those of dx would end last (float32, 2047 x 768 x
+// 1536: 118 us, in two parts 102, two launches 117).
 Plan plan_pair(const ProductArgs& a, const Plan& dx, const Plan& dw) {
   const Sizes x = sizes_of(a, kDx), w = sizes_of(a, kDw);
-  Plan q = {kStream, 1, dx.us + dw.us + 2.0};
+  Plan q = {kStream, 1, dx.us + dw.us + 5.0};  // (a launch's start)
   const int pair = forced("SSM_FORCE_PRODUCT_PAIR"), shape = forced("SSM_FORCE_PRODUCT_SHAPE"),
             parts = forced("SSM_FORCE_PRODUCT_PARTS");
   if (pair == 0 || (pair < 0 && (shape >= 0 || dx.parts > 1))) return q;
@@ -1182,10 +1183,14 @@ Plan plan_pair(const ProductArgs& a, const Plan& dx, const Plan& dw) {
     if (x.tiles(kSides[s]) > kMostTiles) continue;
     const int full = s == kTile64 ? 4 : s == kTile128 ? 2 : 1;  // tiles that a CU works on at once
     for (int t = 1; t <= kMostParts && t <= w.blocks && w.tiles(kSides[s]) * t <= kMostTiles; ++t) {
-      const double one = block_us(s, 1), own = div_up64(w.blocks, t) + kExtra, other = x.blocks + kExtra;
-      const double shared = (w.tiles(kSides[s]) * t * own + x.tiles(kSides[s]) * other) / kCus *
-                                block_us(s, full) / full + 0.5 * other * one;
-      const double us = (shared > own * one ? shared : own * one) + w.join_us(t);
+      const int64_t tiles_w = w.tiles(kSides[s]) * t, tiles_x = x.tiles(kSides[s]);
+      const double own = div_up64(w.blocks, t) + kExtra, other = x.blocks + kExtra;
+      const double shared = (tiles_w * own + tiles_x * other) / kCus * block_us(s, full) / full +
+                            0.5 * other * block_us(s, 1) / full;
+      // the longest takes so long among the others of its CU
+      const int64_t most = div_up64(tiles_w + tiles_x, kCus);
+      const double alone = own * block_us(s, most < full ? most : full);
+      const double us = (shared > alone ? shared : alone) + w.join_us(t);
       if (us < q.us || (pair > 0 && q.shape == kStream)) q = {s, t, us};
     }
   }
