@@ -746,22 +746,6 @@ __global__ __launch_bounds__(64 * WN * WM, 2) void product_kernel(TileArgs p) {
   product_tile<MODE, SIDE, SIDE, WN, WM>(p, blockIdx.x, blockIdx.y, s_a0, s_a1, s_b0, s_b1);
 }
 
-// Both products of the gradient by one launch: first the tiles of dw, `each` workgroups (a
-// multiple of the XCDs) for every part, then those of dx, which fill the CUs that the last of
-// the others leave free.
-template <int SIDE, int WN, int WM>
-__global__ __launch_bounds__(64 * WN * WM, 2) void pair_kernel(TileArgs w, TileArgs x, int64_t each) {
-  SSM_PRODUCT_LDS(SIDE);
-  const int64_t bid = blockIdx.x, behind = bid - each * w.parts;
-  if (behind < 0) {
-    const int part = static_cast<int>(bid / each);
-    product_tile<kDw, SIDE, SIDE, WN, WM>(w, bid - part * each, part, s_a0, s_a1, s_b0, s_b1);
-  } else {
-    product_tile<kDx, SIDE, SIDE, WN, WM>(x, behind, 0, s_a0, s_a1, s_b0, s_b1);
-  }
-}
-#undef SSM_PRODUCT_LDS
-
 // Joins the parts of a product whose summed axis was split, in order, four columns a
 // thread.  limit: the last expert's end, past which rows stay as they are (nullable).
 struct JoinArgs {
@@ -1042,13 +1026,12 @@ __global__ __launch_bounds__(256) void bend_kernel(BendArgs p) {
   }
 }
 
-// dbias[e] = the sum of the expert's tiles, 64 columns a workgroup, its waves
-// the tiles in turn.
-__global__ __launch_bounds__(1024) void bias_kernel(BendArgs p, float* dbias) {
-  __shared__ float s_part[16][64];
+// dbias[e] = the sum of the expert's tiles: columns 64 block .. + 63, by `waves` waves.  The tiles
+// are added in 16 strands and these in turn, however many waves there are.
+__device__ __forceinline__ void bias_columns(const BendArgs& p, float* dbias, int64_t block, int expert,
+                                             int waves, float (*s_part)[64]) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int expert = blockIdx.y;
-  const int64_t width = is_gated(p.act) ? 2 * p.n : p.n, c = static_cast<int64_t>(blockIdx.x) * 64 + lane;
+  const int64_t width = is_gated(p.act) ? 2 * p.n : p.n, c = block * 64 + lane;
   const Tiles tiles = {p.offsets, p.experts, p.rows, p.tile};
   int64_t from = 0, count = (p.rows + p.tile - 1) / p.tile;
   if (p.offsets) {
@@ -1059,19 +1042,54 @@ __global__ __launch_bounds__(1024) void bias_kernel(BendArgs p, float* dbias) {
     }
     if (from + count > p.max_tiles) count = p.max_tiles > from ? p.max_tiles - from : 0;
   }
-  float sum = 0.0f;
-  if (c < width)
+  for (int strand = wave; strand < 16; strand += waves) {
+    float sum = 0.0f;
+    if (c < width)
 #pragma unroll 4
-    for (int64_t t = from + wave; t < from + count; t += 16) sum += p.part[t * width + c];
-  s_part[wave][lane] = sum;
+      for (int64_t t = from + strand; t < from + count; t += 16) sum += p.part[t * width + c];
+    s_part[strand][lane] = sum;
+  }
   __syncthreads();
   if (wave == 0 && c < width) {
-    sum = 0.0f;
+    float sum = 0.0f;
 #pragma unroll
     for (int w = 0; w < 16; ++w) sum += s_part[w][lane];
     dbias[expert * width + c] = sum;
   }
 }
+
+__global__ __launch_bounds__(1024) void bias_kernel(BendArgs p, float* dbias) {
+  __shared__ float s_part[16][64];
+  bias_columns(p, dbias, blockIdx.x, blockIdx.y, 16, s_part);
+}
+
+// Both products of the gradient by one launch, and the last sums of the bias': first the tiles of
+// dw, `each` workgroups (a multiple of the XCDs) for every part, then those of dx up to workgroup
+// `end`, which fill the CUs that the last of the others leave free, then `groups` workgroups an expert
+// for dbias (5 us as a launch of its own).
+struct PairArgs {
+  TileArgs w, x;
+  BendArgs bend;
+  float* dbias;
+  int64_t each, end, groups;
+};
+
+template <int SIDE, int WN, int WM>
+__global__ __launch_bounds__(64 * WN * WM, 2) void pair_kernel(PairArgs p) {
+  SSM_PRODUCT_LDS(SIDE);
+  const int64_t bid = blockIdx.x, behind = bid - p.each * p.w.parts;
+  if (behind < 0) {
+    const int part = static_cast<int>(bid / p.each);
+    product_tile<kDw, SIDE, SIDE, WN, WM>(p.w, bid - part * p.each, part, s_a0, s_a1, s_b0, s_b1);
+  } else if (bid < p.end) {
+    product_tile<kDx, SIDE, SIDE, WN, WM>(p.x, behind, 0, s_a0, s_a1, s_b0, s_b1);
+  } else {
+    const int expert = static_cast<int>((bid - p.end) / p.groups);
+    bias_columns(p.bend, p.dbias, bid - p.end - expert * p.groups, expert, WN * WM,
+                 reinterpret_cast<float (*)[64]>(s_a0));
+  }
+}
+#undef SSM_PRODUCT_LDS
 
 // ---- plans ----
 
@@ -1232,16 +1250,17 @@ void launch_tiles(const TileArgs& t, int shape, hipStream_t stream) {
 }
 
 template <int SIDE, int WN, int WM>
-void launch_pair_side(const TileArgs& w, const TileArgs& x, hipStream_t stream) {
-  const int64_t each = div_up64(grid_of<kDw, SIDE>(w), 8) * 8;
-  const unsigned grid = static_cast<unsigned>(each * w.parts + grid_of<kDx, SIDE>(x));
-  pair_kernel<SIDE, WN, WM><<<grid, 64 * WN * WM, 0, stream>>>(w, x, each);
+void launch_pair_side(PairArgs& p, hipStream_t stream) {
+  p.each = div_up64(grid_of<kDw, SIDE>(p.w), 8) * 8;
+  p.end = p.each * p.w.parts + grid_of<kDx, SIDE>(p.x);
+  const int64_t sums = p.dbias ? p.groups * (p.w.offsets ? p.w.experts : 1) : 0;
+  pair_kernel<SIDE, WN, WM><<<static_cast<unsigned>(p.end + sums), 64 * WN * WM, 0, stream>>>(p);
 }
 
-void launch_pair(const TileArgs& w, const TileArgs& x, int shape, hipStream_t stream) {
-  if (shape == kTile256) launch_pair_side<256, 2, 4>(w, x, stream);
-  else if (shape == kTile128) launch_pair_side<128, 2, 2>(w, x, stream);
-  else launch_pair_side<64, 2, 2>(w, x, stream);
+void launch_pair(PairArgs& p, int shape, hipStream_t stream) {
+  if (shape == kTile256) launch_pair_side<256, 2, 4>(p, stream);
+  else if (shape == kTile128) launch_pair_side<128, 2, 2>(p, stream);
+  else launch_pair_side<64, 2, 2>(p, stream);
 }
 
 template <int MT>
@@ -1371,8 +1390,9 @@ hipError_t SSM_TYPED(launch_product_bwd)(const ProductArgs& a, hipStream_t strea
   const int64_t nw = a.nw();
   const int32_t* offsets = a.experts ? a.offsets : nullptr;
   const void* dpre = a.dout;
+  BendArgs b = {};
+  const int64_t sums = div_up64(nw, 64);  // workgroups an expert for dbias
   if (l.bend) {
-    BendArgs b = {};
     b.dout = a.dout;
     b.pre = a.pre;
     b.dpre = l.dpre ? work : nullptr;
@@ -1388,9 +1408,9 @@ hipError_t SSM_TYPED(launch_product_bwd)(const ProductArgs& a, hipStream_t strea
     const dim3 grid(static_cast<unsigned>(l.tiles), static_cast<unsigned>(div_up64(a.n, 512)));
     if (a.out_dtype == 0) bend_kernel<float><<<grid, 256, 0, stream>>>(b);
     else bend_kernel<bf16_t><<<grid, 256, 0, stream>>>(b);
-    if (l.bias) {
-      const dim3 sums(static_cast<unsigned>(div_up64(nw, 64)), a.experts ? a.experts : 1);
-      bias_kernel<<<sums, 1024, 0, stream>>>(b, a.dbias);
+    if (l.bias && !l.pair) {
+      const dim3 grid(static_cast<unsigned>(sums), a.experts ? a.experts : 1);
+      bias_kernel<<<grid, 1024, 0, stream>>>(b, a.dbias);
     }
     if (l.dpre) dpre = work;
   }
@@ -1420,7 +1440,10 @@ hipError_t SSM_TYPED(launch_product_bwd)(const ProductArgs& a, hipStream_t strea
   w.out = a.dw;
   w.parts = l.dw.parts;
   w.part_stride = matrices * nw * a.k;
-  if (l.pair) launch_pair(w, x, l.dw.shape, stream);
+  if (l.pair) {
+    PairArgs p = {w, x, b, a.dbias, 0, 0, sums};
+    launch_pair(p, l.dw.shape, stream);
+  }
   if (a.dx && !l.pair) {
     launch_tiles<kDx>(x, l.dx.shape, stream);
     if (x.parts > 1) launch_join(x, a.rows, true, kNoAct, stream);
