@@ -8,7 +8,11 @@
 namespace ssm {
 
 // Runs of 8 values.  L lanes hold a row, each every L-th run of it; WHOLE: rows are
-// a whole number of runs.
+// a whole number of runs.  Memory bounds all three, and a wave a row (16 lanes up to 128
+// values) keeps eight or more loads of 16 bytes in flight a lane: 32768 tokens' 4 rows each of 2560 bfloat16
+// into the order 195 us (168 MB read four times, three of them from the caches, 671 MB written:
+// 163 us at a copy's rate), back onto float32 246 to 269 us by card (1.34 GB: 260), gradient of
+// 8191 x 2 x 1536 float32 56 (253 MB: 49).
 
 template <typename T, bool WHOLE>
 __device__ __forceinline__ void load8(Run8<T>& run, const T* p, int left) {

@@ -154,6 +154,16 @@ struct Tiles {
 // block's rows of the summed axis after another, and is transposed on the way to
 // the registers, 4 rows by 16 columns at a time (bfloat16), or read value by value
 // (float32).
+//
+// The matrix instruction bounds a large product.  256 x 256 tiles, eight waves of 128 x
+// 64, read an operand's value from LDS 2 or 4 times and move 64 KB a block for 0.6 us of
+// products: bfloat16 32768 x 5120 x 2560 with silu 720 to 780 us by card (1.1 to 1.2 PFLOP/s;
+// the library's product alone 558 to 746), the pipes busy in 55% of the cycles at 1.73
+// GHz, which is what the card's power allows.  Four waves of 128 x 128 read half as much from LDS:
+// 3 to 5% faster forward, 4 to 12% slower for dw, with the accumulators pinned by hand.  float32
+// keeps 2.1 GHz; 64 x 64 tiles, four workgroups a CU, fill 76% of the cycles, 128 x 128
+// 82% (11686 x 1344 x 2960 767 us, the library 773).  Two buffers: four or five slots of
+// a ring gained nothing, since a CU's other waves work through a wait.
 enum Mode { kFwd, kGlu, kDx, kDw };
 
 struct TileArgs {
@@ -811,7 +821,7 @@ __global__ __launch_bounds__(256) void join_kernel(JoinArgs p) {
 // straight into the matrix instruction's registers: a workgroup takes 16 rows of one
 // matrix (of a gated one 16 of either half), its waves the blocks of 128 bytes in
 // turn; the activations come from the L2.  The waves' sums meet in LDS and are added
-// in wave order.  A matrix with more than 16 MT rows is read again for the next ones.
+// in wave order.  A matrix with more than 16 rows is read again for the next ones.
 //
 // Two workgroups a CU, 16 waves, keep the reads in flight: with three registers more
 // than 128 a lane it is one, and 8 tokens' rows of 4 of 64 experts (2560 -> 2 x 1280 gated,
@@ -820,10 +830,10 @@ __global__ __launch_bounds__(256) void join_kernel(JoinArgs p) {
 // reach their rate: 10.8 us.
 constexpr int kStreamWaves = 8;
 
-template <int MT, bool GLU>
+template <bool GLU>
 __global__ __launch_bounds__(64 * kStreamWaves, 4) void stream_kernel(TileArgs p) {
   constexpr int H = GLU ? 2 : 1;
-  __shared__ f32x4 s_sum[kStreamWaves][H * MT][64];
+  __shared__ f32x4 s_sum[kStreamWaves][H][64];
   const int lane = threadIdx.x & 63, i = lane & 15, quad = lane >> 4;
   const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int W = blockDim.x >> 6;
@@ -866,55 +876,44 @@ __global__ __launch_bounds__(64 * kStreamWaves, 4) void stream_kernel(TileArgs p
     }
     return v;
   };
-  for (int64_t m0 = range.from; m0 < range.to; m0 += 16 * MT) {
-    const char* xrow[MT];
-    bool in[MT];
-#pragma unroll
-    for (int m = 0; m < MT; ++m) {
-      const int64_t r = m0 + m * 16 + i;
-      int64_t t = r < range.to ? r : range.to - 1;
-      in[m] = true;
-      if (p.token) {
-        t = p.token[t];
-        in[m] = t >= 0 && t < p.x_rows;
-      }
-      xrow[m] = static_cast<const char*>(p.b) + (in[m] ? t : 0) * p.ldb * kSize;
+  for (int64_t m0 = range.from; m0 < range.to; m0 += 16) {
+    const int64_t r = m0 + i;
+    int64_t t = r < range.to ? r : range.to - 1;
+    bool in = true;
+    if (p.token) {
+      t = p.token[t];
+      in = t >= 0 && t < p.x_rows;
     }
-    f32x4 acc[H][MT] = {};
-    constexpr int U = MT * H == 1 ? 4 : 2;  // blocks in flight
+    const char* xrow = static_cast<const char*>(p.b) + (in ? t : 0) * p.ldb * kSize;
+    f32x4 acc[H] = {};
+    constexpr int U = GLU ? 2 : 4;  // blocks in flight
     for (int g0 = w; g0 < groups; g0 += U * W) {
-      i32x8 a[U][H], b[U][MT];
+      i32x8 a[U][H], b[U];
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         const int at = (g0 + u * W) * kBlockBytes + quad * 16;
 #pragma unroll
         for (int h = 0; h < H; ++h) a[u][h] = load32(wrow[h], at);
-#pragma unroll
-        for (int m = 0; m < MT; ++m) b[u][m] = load32(xrow[m], in[m] ? at : bytes);
+        b[u] = load32(xrow, in ? at : bytes);
       }
 #pragma unroll
       for (int u = 0; u < U; ++u)
 #pragma unroll
         for (int s = 0; s < kSteps; ++s)
 #pragma unroll
-          for (int h = 0; h < H; ++h)
-#pragma unroll
-            for (int m = 0; m < MT; ++m) acc[h][m] = mfma(a[u][h], b[u][m], s, acc[h][m]);
+          for (int h = 0; h < H; ++h) acc[h] = mfma(a[u][h], b[u], s, acc[h]);
     }
 #pragma unroll
-    for (int h = 0; h < H; ++h)
-#pragma unroll
-      for (int m = 0; m < MT; ++m) s_sum[w][h * MT + m][lane] = acc[h][m];
+    for (int h = 0; h < H; ++h) s_sum[w][h][lane] = acc[h];
     __syncthreads();
-    for (int m = w; m < MT; m += W) {
+    const int64_t c = c0 + quad * 4;
+    if (w == 0 && r < range.to && c < p.cols) {
       f32x4 v[H];
 #pragma unroll
       for (int h = 0; h < H; ++h) {
-        v[h] = s_sum[0][h * MT + m][lane];
-        for (int q = 1; q < W; ++q) v[h] += s_sum[q][h * MT + m][lane];
+        v[h] = s_sum[0][h][lane];
+        for (int q = 1; q < W; ++q) v[h] += s_sum[q][h][lane];
       }
-      const int64_t r = m0 + m * 16 + i, c = c0 + quad * 4;
-      if (r >= range.to || c >= p.cols) continue;
       const int last = p.cols - c < 4 ? static_cast<int>(p.cols - c) - 1 : 3;
 #pragma unroll
       for (int h = 0; h < H; ++h) {
@@ -941,7 +940,9 @@ __global__ __launch_bounds__(64 * kStreamWaves, 4) void stream_kernel(TileArgs p
 //
 // dpre in the activations' type for the two products, and its sums over the rows of
 // each tile of p.tile rows of an expert from the values before that rounding.  A wave
-// takes 512 columns, 8 a lane, of every fourth row.
+// takes 512 columns, 8 a lane, of every fourth row.  Memory bounds it: 16384 x 5120 bfloat16
+// of a gelu or silu 91 us (503 MB, 5.5 TB/s), 16384 rows of 16 experts, 2 x 2560 gated, 84.  In the
+// products themselves it would be done once for every tile of the other axis.
 
 struct BendArgs {
   const void *dout, *pre;
@@ -953,8 +954,9 @@ struct BendArgs {
   int64_t ld;               // of dpre's rows: nw, up to the next multiple of 8; zeros past nw
 };
 
-// Rows of a tile: few where that leaves the CUs without work.
-int bend_rows(int64_t rows, int64_t n) { return rows * n < (1 << 23) ? 32 : 128; }
+// Rows of a tile: few where 128 would leave the CUs without work (bias alone: 2047 x 768 float32
+// 4.3 us by 32 rows, 8.0 by 128, 2047 x 5120 bfloat16 5.8 and 10.5, 16384 x 5120 28 and 25).
+int bend_rows(int64_t rows, int64_t n) { return rows * n < (1 << 25) ? 32 : 128; }
 
 template <typename D>
 __global__ __launch_bounds__(256) void bend_kernel(BendArgs p) {
@@ -1111,7 +1113,6 @@ int whole_parts(int64_t blocks, int parts) {
   return parts <= 1 ? 1 : static_cast<int>(div_up64(blocks, div_up64(blocks, parts)));
 }
 
-constexpr int kStreamRows = 32;
 constexpr int64_t kCus = 256;
 
 // Most tiles of `side` rows that `rows` rows of the experts make: each expert's last
@@ -1145,8 +1146,10 @@ double block_us(int shape, int64_t n) {
 // 128 x 128 ones, bfloat16 4096 x 5120 x 2560 126 and 116; bfloat16 2048 x 5120 x 2560 60
 // (160 tiles, one round) and 79.  Few tiles with a long sum are split: bfloat16, the rows'
 // gradient of 1024 x 5120 x 2560 takes 64 us by 160 tiles of 128 x 128, 48 by two parts of each.
-// kStreamRows rows or fewer of a matrix: every wave would read the weights for a tile of
-// rows that are mostly padding, and the stream kernel reads them straight into registers.
+// Few rows of a matrix take the stream kernel: 16 bfloat16 rows x 5120 x 2560 12.8 us, 13.7 by 64 x 64
+// tiles in parts, 24 rows 15.2 and 13.6.  Experts' rows differ in number, and one with more
+// than 16 has its weights read twice: 64 experts of 2 x 1280 x 2560 with 8 rows at the mean 156 us,
+// 160 by tiles, with 16 205 and 163; float32 346 and 375, 491 and 379.
 struct Sizes {  // of a product in tiles
   int64_t high, cols, blocks, matrices;
   int64_t tiles(int64_t side) const { return matrices * div_up64(high, side) * div_up64(cols, side); }
@@ -1165,7 +1168,7 @@ constexpr int kExtra = kSize == 4 ? 2 : 5;  // blocks a tile, its start and its 
 Plan plan_tiles(const ProductArgs& a, int mode) {
   const Sizes z = sizes_of(a, mode);
   Plan q = {kTile64, 1, 0.0};
-  if ((mode == kFwd || mode == kGlu) && z.high <= kStreamRows) q.shape = kStream;
+  if ((mode == kFwd || mode == kGlu) && z.high <= (a.experts ? 8 : 16)) q.shape = kStream;
   for (int s = kTile64; s <= kTile256 && q.shape != kStream; ++s) {
     const int64_t all = z.tiles(kSides[s]);
     if (all > kMostTiles && s != kTile256) continue;
@@ -1263,14 +1266,13 @@ void launch_pair(PairArgs& p, int shape, hipStream_t stream) {
   else launch_pair_side<64, 2, 2>(p, stream);
 }
 
-template <int MT>
 void launch_stream(const TileArgs& t, bool glu, hipStream_t stream) {
   const int64_t groups = div_up64(t.depth * kSize, kBlockBytes);
   const int waves = static_cast<int>(div_up64(groups, div_up64(groups, kStreamWaves)));
   const int64_t y = !t.offsets ? 1 : t.rows < t.experts ? t.rows : t.experts;
   const dim3 grid(static_cast<unsigned>(div_up64(t.cols, 16)), static_cast<unsigned>(y));
-  if (glu) stream_kernel<MT, true><<<grid, 64 * waves, 0, stream>>>(t);
-  else stream_kernel<MT, false><<<grid, 64 * waves, 0, stream>>>(t);
+  if (glu) stream_kernel<true><<<grid, 64 * waves, 0, stream>>>(t);
+  else stream_kernel<false><<<grid, 64 * waves, 0, stream>>>(t);
 }
 
 void launch_join(const TileArgs& t, int64_t rows, bool of_rows, int act, hipStream_t stream) {
@@ -1373,9 +1375,7 @@ hipError_t SSM_TYPED(launch_product_fwd)(const ProductArgs& a, hipStream_t strea
   t.part = static_cast<float*>(a.work);
   t.part_stride = a.rows * a.nw();
   if (q.shape == kStream) {
-    // (the fewest rows that any matrix can have to be sure; of experts' the mean is far below)
-    if (a.rows <= (a.experts > 2 ? 8 * a.experts : 16)) launch_stream<1>(t, glu, stream);
-    else launch_stream<2>(t, glu, stream);
+    launch_stream(t, glu, stream);
   } else {
     if (glu) launch_tiles<kGlu>(t, q.shape, stream);
     else launch_tiles<kFwd>(t, q.shape, stream);
