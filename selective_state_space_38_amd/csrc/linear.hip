@@ -1139,17 +1139,6 @@ double block_us(int shape, int64_t n) {
   return 0.72 * (n / 4) + (n % 4 ? 0.45 + 0.05 * (n % 4) : 0.0);
 }
 
-// The tile and the parts of the summed axis of the least cost: what the fullest CU has
-// to do, and for parts the join, 4 us and its traffic at 5 TB/s.  The largest tile moves
-// the least memory, but 276 of them keep 256 CUs for two rounds, the second nearly
-// empty: float32, 11686 rows x 1344 x 2960 takes 1469 us by 256 x 256 tiles and 768 by
-// 128 x 128 ones, bfloat16 4096 x 5120 x 2560 126 and 116; bfloat16 2048 x 5120 x 2560 60
-// (160 tiles, one round) and 79.  Few tiles with a long sum are split: bfloat16, the rows'
-// gradient of 1024 x 5120 x 2560 takes 64 us by 160 tiles of 128 x 128, 48 by two parts of each.
-// Few rows of a matrix take the stream kernel: 16 bfloat16 rows x 5120 x 2560 12.8 us, 13.7 by 64 x 64
-// tiles in parts, 24 rows 15.2 and 13.6.  Experts' rows differ in number, and one with more
-// than 16 has its weights read twice: 64 experts of 2 x 1280 x 2560 with 8 rows at the mean 156 us,
-// 160 by tiles, with 16 205 and 163; float32 346 and 375, 491 and 379.
 struct Sizes {  // of a product in tiles
   int64_t high, cols, blocks, matrices;
   int64_t tiles(int64_t side) const { return matrices * div_up64(high, side) * div_up64(cols, side); }
@@ -1165,6 +1154,18 @@ Sizes sizes_of(const ProductArgs& a, int mode) {
 constexpr int kSides[] = {0, 64, 128, 256};
 constexpr int kExtra = kSize == 4 ? 2 : 5;  // blocks a tile, its start and its epilogue
 
+// The tile and the parts of the summed axis of the least cost: what the fullest CU has
+// to do, and for parts the join, 4 us and its traffic at 5 TB/s.  The largest tile moves
+// the least memory, but 276 of them keep 256 CUs for two rounds, the second nearly
+// empty: float32, 11686 rows x 1344 x 2960 takes 1469 us by 256 x 256 tiles and 768 by
+// 128 x 128 ones, bfloat16 4096 x 5120 x 2560 126 and 116; bfloat16 2048 x 5120 x 2560 60
+// (160 tiles, one round) and 79.  Few tiles with a long sum are split: bfloat16, the rows'
+// gradient of 1024 x 5120 x 2560 takes 64 us by 160 tiles of 128 x 128, 48 by two parts of each.
+// Few rows of a matrix take the stream kernel: 16 bfloat16 rows x 5120 x 2560 12.9 us, 14.6 by 64 x 64
+// tiles in parts, 24 rows, for which it reads the weights twice, 20.9 and 15.0.  Experts' rows
+// differ in number: 64 experts of 2 x 1280 x 2560 with 8 rows at the mean 157 us, 160 by tiles,
+// with 16 237 and 163; float32 345 and 373, 540 and 382.  SSM_FORCE_PRODUCT_SHAPE and
+// _PARTS override (tests, tuning), for the gradient SSM_FORCE_PRODUCT_PAIR.
 Plan plan_tiles(const ProductArgs& a, int mode) {
   const Sizes z = sizes_of(a, mode);
   Plan q = {kTile64, 1, 0.0};
