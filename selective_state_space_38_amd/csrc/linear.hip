@@ -1128,12 +1128,13 @@ constexpr int kMostParts = 32;
 // What one block of the summed axis takes on a CU that has `n` tiles of this shape to
 // do, in us, for all of them: the figures of products that fill 1 to 40 tiles a CU, within
 // a tenth of the measured times with 2 blocks (float32) or 5 (bfloat16) added a tile for
-// its start and its epilogue.  A float32 tile keeps the matrix units busy by itself, so
-// that tiles of one CU add up; a bfloat16 tile waits for its loads, and a second of
-// 128 x 128 or three more of 64 x 64 run meanwhile.
+// its start and its epilogue.  A float32 tile all but fills the matrix units by itself, so
+// that tiles of one CU add up (a second of 128 x 128 gains an eighth); a bfloat16 tile waits
+// for its loads, and a second of 128 x 128 or three more of 64 x 64 run meanwhile.
 double block_us(int shape, int64_t n) {
   const double d = static_cast<double>(n);
-  if (kSize == 4) return d * (shape == kTile256 ? 7.9 : shape == kTile128 ? 2.06 : 0.56);
+  if (kSize == 4 && shape == kTile128) return 3.95 * (n / 2) + 2.25 * (n % 2);
+  if (kSize == 4) return d * (shape == kTile256 ? 7.9 : 0.56);
   if (shape == kTile256) return 1.4 * d;
   if (shape == kTile128) return 0.9 * (n / 2) + 0.75 * (n % 2);
   return 0.72 * (n / 4) + (n % 4 ? 0.45 + 0.05 * (n % 4) : 0.0);
@@ -1143,7 +1144,7 @@ struct Sizes {  // of a product in tiles
   int64_t high, cols, blocks, matrices;
   int64_t tiles(int64_t side) const { return matrices * div_up64(high, side) * div_up64(cols, side); }
   double join_us(int parts) const {
-    return parts > 1 ? 4.0 + 8e-6 / 5.0 * static_cast<double>(matrices) * high * cols * parts : 0.0;
+    return parts > 1 ? 6.0 + 8e-6 / 10.0 * static_cast<double>(matrices) * high * cols * parts : 0.0;
   }
 };
 Sizes sizes_of(const ProductArgs& a, int mode) {
@@ -1155,7 +1156,7 @@ constexpr int kSides[] = {0, 64, 128, 256};
 constexpr int kExtra = kSize == 4 ? 2 : 5;  // blocks a tile, its start and its epilogue
 
 // The tile and the parts of the summed axis of the least cost: what the fullest CU has
-// to do, and for parts the join, 4 us and its traffic at 5 TB/s.  The largest tile moves
+// to do, and for parts the join, 6 us and its traffic at 10 TB/s (the parts are still in a cache).  The largest tile moves
 // the least memory, but 276 of them keep 256 CUs for two rounds, the second nearly
 // empty: float32, 11686 rows x 1344 x 2960 takes 1469 us by 256 x 256 tiles and 768 by
 // 128 x 128 ones, bfloat16 4096 x 5120 x 2560 126 and 116; bfloat16 2048 x 5120 x 2560 60
@@ -1208,10 +1209,11 @@ Plan plan_pair(const ProductArgs& a, const Plan& dx, const Plan& dw) {
       const int64_t tiles_w = w.tiles(kSides[s]) * t, tiles_x = x.tiles(kSides[s]);
       const double own = div_up64(w.blocks, t) + kExtra, other = x.blocks + kExtra;
       const double shared = (tiles_w * own + tiles_x * other) / kCus * block_us(s, full) / full +
-                            0.5 * other * block_us(s, 1) / full;
-      // the longest takes so long among the others of its CU
+                            0.5 * other * block_us(s, 1) / (full * full);
+      // the longest takes so long: one of dw among the others of its CU, one of dx with nobody else
       const int64_t most = div_up64(tiles_w + tiles_x, kCus);
-      const double alone = own * block_us(s, most < full ? most : full);
+      const double last = other * block_us(s, 1), first = own * block_us(s, most < full ? most : full);
+      const double alone = first > last ? first : last;
       const double us = (shared > alone ? shared : alone) + w.join_us(t);
       if (us < q.us || (pair > 0 && q.shape == kStream)) q = {s, t, us};
     }
