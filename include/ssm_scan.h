@@ -686,7 +686,10 @@ typedef struct {
  *               value there.  An expert whose logit is -inf is not chosen: where
  *               fewer than topk are left, -1.
  *   weight    : [tokens][topk] float32, scale times the chosen experts' scores,
- *               divided by their sum with renormalize; 0 where index is -1
+ *               divided by their sum with renormalize; 0 where index is -1.  A NaN or
+ *               +inf among a softmax' logits makes all scores of its row NaN, and so
+ *               every weight with an expert, chosen or not; a sigmoid's NaN is its own
+ *               expert's, and with renormalize its choice's row's
  *   score_sum : [experts] float32 (nullable), each expert's scores summed over the
  *               tokens (a row of -inf adds nothing)
  *   work      : expert_route_work_bytes(dims) bytes (nullable without score_sum)

@@ -20,15 +20,17 @@ def _sigmoid(v):
 
 
 def scores(logits, score="softmax"):
-    """Each expert's score, row by row; a row of -inf scores 0 everywhere."""
+    """Each expert's score, row by row; a row of -inf scores 0 everywhere, a softmax' row
+    with a NaN or +inf is NaN everywhere."""
     v = np.asarray(logits, np.float64)
     if score == "sigmoid":
         return _sigmoid(v)
     out = np.zeros_like(v)
     for t, row in enumerate(v):
         top = row.max()
-        if top > -np.inf:
-            e = np.exp(row - top)
+        if top != -np.inf:
+            with np.errstate(invalid="ignore"):
+                e = np.exp(row - top)
             out[t] = e / e.sum()
     return out
 
@@ -46,8 +48,8 @@ def route(logits, k, score="softmax", renormalize=False, scale=1.0):
             if left[e] == -np.inf:
                 break
             index[t, j], weight[t, j], left[e] = e, s[t, e], -np.inf
-        if renormalize and weight[t].sum() > 0:
-            weight[t] /= weight[t].sum()
+        if renormalize and weight[t].sum() != 0:
+            weight[t, index[t] >= 0] /= weight[t].sum()
     return index, scale * weight, s.sum(0)
 
 

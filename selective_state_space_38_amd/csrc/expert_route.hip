@@ -192,6 +192,9 @@ __global__ __launch_bounds__(kRouteThreads) void route_fwd_kernel(RouteArgs p) {
     if (p.renormalize) {
       mine = chosen >= 0 ? S::share(mine, top, p.sigmoid) : 0.0f;
       sum = S::all_sum(mine);
+      // the shares know the chosen logits alone: another one that is not a number, or +inf,
+      // leaves no score of a softmax
+      if (!p.sigmoid && r.scale != r.scale) sum = r.scale;
     } else {
       mine = r.score_of(mine, p.sigmoid);
     }

@@ -46,7 +46,9 @@ def expert_route_fwd(logits, k, score="softmax", renormalize=False, scale=1.0,
     an expert whose logit is -inf is not chosen, and an entry left without one is
     -1 with weight 0), weight [tokens, k] float32 and, with return_score_sum,
     score_sum [experts] float32, every expert's scores summed over the tokens.
-    At most 1024 experts and 16 choices.
+    A NaN counts as the lowest finite logit in the choice; under a softmax it makes
+    its row's weights NaN, chosen or not (so does +inf), under a sigmoid only where
+    it is chosen.  At most 1024 experts and 16 choices.
     """
     dims = _route_args(logits, k, score, renormalize)
     dev, shape = logits.device, (logits.shape[0], k)
