@@ -703,7 +703,11 @@ int expert_route_fwd(const void* logits, float scale, int32_t* index,
  * Its gradient with respect to logits, of sum dweight*weight + sum
  * dscore_sum*score_sum, with the choice held.
  *   index      : as the forward wrote it (nullable without dweight); an entry
- *                outside 0 .. experts - 1 takes no part
+ *                outside 0 .. experts - 1 takes no part.  With renormalize the
+ *                weights are shares of those that do: where choices are dropped
+ *                behind the forward, expert_sort takes the index without them, this
+ *                the forward's own, with dweight 0 for them as expert_combine_bwd
+ *                gives it
  *   dweight    : [tokens][topk] float32 (nullable = zeros)
  *   dscore_sum : [experts] float32 (nullable = zeros); one of the two is given
  *   dlogits    : [tokens][experts] of dtype
@@ -716,7 +720,8 @@ int expert_route_bwd(const void* logits, float scale, const int32_t* index,
  * The order by expert: rows offsets[e] .. offsets[e + 1] - 1 are expert e's, in
  * the order of (token, choice).  experts at most 1024, topk at most 16 (it may exceed
  * experts: a token may name an expert twice), tokens * topk at most 2^30.
- *   index   : [tokens][topk]; an entry outside 0 .. experts - 1 has no row
+ *   index   : [tokens][topk]; an entry outside 0 .. experts - 1 has no row (a choice
+ *             dropped for want of room, say; expert_route_bwd takes the index with it)
  *   offsets : [experts + 1]
  *   token   : [tokens * topk], the token of every row; -1 past offsets[experts]
  *   slot    : [tokens][topk], the row of every choice; -1 for one without

@@ -72,7 +72,10 @@ def expert_route_bwd(logits, index, dweight, score="softmax", renormalize=False,
     """Backward of expert_route_fwd on the GPU, with the choice held: dlogits, in
     logits' type and shape, from dweight [tokens, k] and dscore_sum [experts]
     (float32; either may be None).  index: what the forward returned (an entry
-    outside the experts takes no part)."""
+    outside the experts takes no part).  With renormalize the weights are shares of
+    the entries that do: where choices are dropped behind the router, give the index
+    without them to expert_sort only, and the forward's own here, with the dweight
+    of expert_combine_bwd, which is 0 for them."""
     if index is None:
         raise ValueError("index is required")
     if dweight is None and dscore_sum is None:
@@ -106,7 +109,7 @@ def expert_sort(index, experts):
     offsets[e + 1] - 1 are expert e's, in the order of (token, choice).
 
     index: [tokens, k] int32; an entry outside 0 .. experts - 1 (a choice that
-    was dropped) has no row.  Returns int32 offsets [experts + 1], token
+    was dropped; expert_route_bwd takes the index with it) has no row.  Returns int32 offsets [experts + 1], token
     [tokens * k] (every row's token; -1 past offsets[experts]) and slot
     [tokens, k] (every choice's row; -1 for one without).
     """
