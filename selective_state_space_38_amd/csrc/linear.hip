@@ -946,7 +946,7 @@ __global__ __launch_bounds__(64 * kStreamWaves, 4) void stream_kernel(TileArgs p
 
 struct BendArgs {
   const void *dout, *pre;
-  void* dpre;               // nullable: dout serves as it is
+  void* dpre;               // nullable: dout serves as it is, or there is no product
   float* part;              // [tiles][nw], nullable
   const int32_t* offsets;
   int experts, act, tile;
@@ -1309,8 +1309,8 @@ struct BwdLayout {
 
 BwdLayout bwd_layout(const ProductArgs& a) {
   BwdLayout l = {};
-  // dout serves as dpre unless its rows are not whole runs of 16 bytes
-  const bool copy = a.act != kNoAct || a.out_dtype != a.dtype || a.n % 8;
+  // the products' dpre; dout serves as it unless its rows are not whole runs of 16 bytes
+  const bool copy = (a.dx || a.dw) && (a.act != kNoAct || a.out_dtype != a.dtype || a.n % 8);
   l.bend = copy || a.dbias;
   l.dpre = copy ? up16(a.rows * ld_dpre(a) * kSize) : 0;
   l.tiles = most_tiles(a.rows, a.experts, bend_rows(a.rows, a.n));
