@@ -734,9 +734,9 @@ int expert_sort(const int32_t* index, int64_t tokens, int32_t topk,
 
 /* Sizes of the way into the order and back: rows of dim values. */
 typedef struct {
-  int64_t tokens;          /* at most 2^25 */
+  int64_t tokens;          /* at most 2^25; tokens * topk at most 2^30 */
   int64_t rows;            /* of xs, y, dy; at most 2^25 */
-  int64_t dim;
+  int64_t dim;             /* at most 2^24 */
   int32_t topk;            /* at most 16 */
   int32_t dtype;           /* ssm_dtype of x, xs, y, dy */
   int32_t residual_dtype;  /* ssm_dtype of residual, out, dout */
@@ -777,14 +777,15 @@ typedef enum {
   SSM_ACT_GEGLU = 4    /* gelu(first half) * second half */
 } ssm_activation;
 
-/* Sizes of a product: nw = n, or 2 n with a gated activation.  Of its outputs, of
- * [rows][k] and of [experts][nw][k] at most 2^21 tiles of 256 x 256. */
+/* Sizes of a product: nw = n, or 2 n with a gated activation.  Of [rows][nw], of [rows][k]
+ * (a tile of rows more for every expert) and of [experts][nw][k] at most 2^21 tiles of
+ * 256 x 256. */
 typedef struct {
   int64_t rows;
-  int64_t n;            /* columns of out */
-  int64_t k;            /* columns of x; a multiple of 8 */
-  int64_t x_rows;       /* rows of x: rows without token */
-  int64_t ld_x;         /* elements between x's rows, >= k, a multiple of 8 */
+  int64_t n;            /* columns of out; at most 2^20 */
+  int64_t k;            /* columns of x; a multiple of 8, at most 2^20 */
+  int64_t x_rows;       /* rows of x: rows without token; at most 2^30 */
+  int64_t ld_x;         /* elements between x's rows, >= k, a multiple of 8, at most 2^26 */
   int32_t experts;      /* 0: one matrix for all rows; at most 1024 */
   int32_t activation;   /* ssm_activation */
   int32_t dtype;        /* ssm_dtype of x, w, pre, dx, dw */

@@ -100,8 +100,6 @@ int check_product(const product_dims* d) {
   if (row_tiles * ssm::div_up64(nw > d->k ? nw : d->k, 256) > ssm::kMostTiles) return SSM_EINVAL;
   const int64_t matrices = d->experts ? d->experts : 1;
   if (matrices * ssm::div_up64(nw, 256) * ssm::div_up64(d->k, 256) > ssm::kMostTiles) return SSM_EINVAL;
-  if (d->rows * ssm::div_up64(nw > d->k ? nw : d->k, 1024) > (1LL << 31) - 1) return SSM_EINVAL;
-  if (matrices * nw * ssm::div_up64(d->k, 1024) > (1LL << 31) - 1) return SSM_EINVAL;
   return SSM_OK;
 }
 
