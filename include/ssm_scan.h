@@ -801,8 +801,9 @@ typedef struct {
  *   x        : [x_rows][k], row stride ld_x
  *   token    : [rows] (nullable; only with experts)
  *   w        : [experts][nw][k]  ([nw][k] with experts 0)
- *   offsets  : [experts + 1], from 0, none less than the one before (NULL with
- *              experts 0).  Rows from offsets[experts] on are left as they are.
+ *   offsets  : [experts + 1], none less than the one before (NULL with experts 0).
+ *              Rows ahead of offsets[0] and from offsets[experts] on are left as they
+ *              are (a run of an order's experts takes that run of its offsets).
  *   bias     : [experts][nw] float32 (nullable)
  *   residual : [rows][n] of out_dtype (nullable); out may be residual itself
  *   out      : [rows][n] of out_dtype
@@ -827,8 +828,8 @@ int linear_fwd(const void* x, const int32_t* token, const void* w,
  *   dbias[e] = sum_r dpre[r], r over the expert's rows.
  *   pre   : as the forward wrote it; NULL without activation
  *   dx    : [rows][k] of dtype (nullable), by row, not by token: with token its rows
- *           are summed by expert_combine_fwd.  Rows past the last expert's are left
- *           as they are.
+ *           are summed by expert_combine_fwd.  Rows of no expert are left as they
+ *           are.
  *   dw    : as w (nullable);  dbias : [experts][nw] float32 (nullable); zeros for an
  *           expert without rows
  *   work  : linear_bwd_work_bytes(dims, the SSM_WANT_ bits of those given) bytes

@@ -757,14 +757,13 @@ __global__ __launch_bounds__(64 * WN * WM, 2) void product_kernel(TileArgs p) {
 }
 
 // Joins the parts of a product whose summed axis was split, in order, four columns a
-// thread.  limit: the last expert's end, past which rows stay as they are (nullable).
+// thread.  Rows ahead of the first expert's and past the last one's stay as they are.
 struct JoinArgs {
   const float* part;
   int parts, act;
   bool out_f32;
   int64_t part_stride, rows, cols;  // cols: of out
-  const int32_t* limit;
-  const int32_t* offsets;           // of the bias' experts, nullable
+  const int32_t* offsets;           // of the experts that have the rows, nullable
   int experts;
   const float* bias;
   const void* residual;
@@ -774,7 +773,7 @@ struct JoinArgs {
 __global__ __launch_bounds__(256) void join_kernel(JoinArgs p) {
   const int64_t quads = (p.cols + 3) / 4, at = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
   const int64_t row = at / quads, c = (at - row * quads) * 4;
-  if (row >= p.rows || (p.limit && row >= *p.limit)) return;
+  if (row >= p.rows || (p.offsets && (row < p.offsets[0] || row >= p.offsets[p.experts]))) return;
   const bool glu = is_gated(p.act);
   const int64_t width = glu ? 2 * p.cols : p.cols;
   const int last = p.cols - c < 4 ? static_cast<int>(p.cols - c) - 1 : 3;
@@ -1287,7 +1286,6 @@ void launch_join(const TileArgs& t, int64_t rows, bool of_rows, int act, hipStre
   j.part_stride = t.part_stride;
   j.rows = rows;
   j.cols = t.cols;
-  j.limit = of_rows && t.offsets ? t.offsets + t.experts : nullptr;
   j.offsets = of_rows ? t.offsets : nullptr;
   j.experts = t.offsets ? t.experts : 0;
   j.bias = t.bias;

@@ -371,7 +371,8 @@ def expert_linear_fwd(x, w, offsets, token=None, bias=None, activation=None, ret
     expert_sort returns them.  With token row r of the product is x's row
     token[r] (zeros where that is none), so the tokens need no copy in the
     experts' order; without, x holds the rows in order.  bias: [experts, n]
-    float32.  Returns out [rows, n], or (out, pre); rows from offsets[experts] on
+    float32.  Returns out [rows, n], or (out, pre); rows ahead of offsets[0] (of a run
+    of the order's experts, w[a:b] with offsets[a:b + 1]) and from offsets[experts] on
     are left as they are (give out to choose what).
     """
     _need_offsets(offsets)
@@ -385,7 +386,7 @@ def expert_linear_bwd(dout, x, w, offsets, token=None, activation=None, pre=None
     dout: [rows, n], the gradient of out; the rest as in the forward and in
     linear_bwd.  Returns a dict of those asked for: dx [rows, k], the gradient of
     every row in the experts' order (with token, expert_combine_fwd(dx, slot) sums
-    it by token; rows from offsets[experts] on are left as they are), dw
+    it by token; rows of no expert are left as they are), dw
     [experts, n, k] in x's type and, with bias, dbias [experts, n] float32, zeros
     for an expert without rows.
     """
