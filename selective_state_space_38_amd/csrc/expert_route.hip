@@ -19,7 +19,7 @@ namespace ssm {
 // The instructions of the choice bound it, k rounds of a maximum over V values and L
 // lanes: of bfloat16 logits over one word of value and number, 8.8 us for 32768 tokens of 128
 // experts, k 8 (12.2 by a maximum, a search for its lane and that lane's number, as float32
-// logits need; the logits' 8 MB and what is written take 2.4).  16 lanes a token keep the
+// logits need: theirs take 11.4; the logits' 8 MB and what is written 2.4).  16 lanes a token keep the
 // maximum in one row of the wave, without LDS; from 257 experts on a lane would hold
 // more than 16, and the whole wave takes a token.
 

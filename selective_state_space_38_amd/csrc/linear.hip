@@ -942,6 +942,12 @@ __global__ __launch_bounds__(64 * kStreamWaves, 4) void stream_kernel(TileArgs p
 // takes 512 columns, 8 a lane, of every fourth row.  Memory bounds it: 16384 x 5120 bfloat16
 // of a gelu or silu 91 us (503 MB, 5.5 TB/s), 16384 rows of 16 experts, 2 x 2560 gated, 84.  In the
 // products themselves it would be done once for every tile of the other axis.
+//
+// bfloat16: the matrix instruction takes bfloat16 operands, so dpre is rounded once, also a
+// float32 dout without activation.  Carried as two bfloat16 parts it would double both products.
+// The rounding adds as much as the outputs' own: 2048 x 5120 x 2560, dx and dw are off float64 by
+// 0.0023 of their norm, 0.0017 with dpre in float32.  The bias' sums take it before.
+// Without dx and dw only the sums are written: 16384 x 5120 76 us as a call.
 
 struct BendArgs {
   const void *dout, *pre;
@@ -1164,7 +1170,8 @@ constexpr int kExtra = kSize == 4 ? 2 : 5;  // blocks a tile, its start and its 
 // Few rows of a matrix take the stream kernel: 16 bfloat16 rows x 5120 x 2560 12.9 us, 14.6 by 64 x 64
 // tiles in parts, 24 rows, for which it reads the weights twice, 20.9 and 15.0.  Experts' rows
 // differ in number: 64 experts of 2 x 1280 x 2560 with 8 rows at the mean 157 us, 160 by tiles,
-// with 16 237 and 163; float32 345 and 373, 540 and 382.  SSM_FORCE_PRODUCT_SHAPE and
+// with 16 237 and 163; float32 345 and 373, 540 and 382.  The host knows the mean alone: 512 rows of
+// those 64 experts 157 us, 181 with half of them one expert's, 250 with all (float32 356, 421, 509).  SSM_FORCE_PRODUCT_SHAPE and
 // _PARTS override (tests, tuning), for the gradient SSM_FORCE_PRODUCT_PAIR.
 Plan plan_tiles(const ProductArgs& a, int mode) {
   const Sizes z = sizes_of(a, mode);

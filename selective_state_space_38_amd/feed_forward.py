@@ -352,7 +352,9 @@ def linear_bwd(dout, x, w, activation=None, pre=None, need_dx=True, need_dw=True
     dout: the gradient of out, in out's type; x, w, activation as in the forward;
     pre: what it returned with return_pre, given exactly with an activation.
     Returns a dict of those asked for: dx [..., k] and dw [n, k] in x's type and,
-    with bias, dbias [n] float32.
+    with bias (a truth value), dbias [n] float32.  With an activation, or a dout of
+    another type, the gradient before the activation is rounded to x's type in front
+    of the two products (dbias is summed before that).
     """
     return _linear_bwd(dout, x, w, None, None, activation, pre, need_dx, need_dw, bias, None)
 
