@@ -1171,8 +1171,9 @@ constexpr int kExtra = kSize == 4 ? 2 : 5;  // blocks a tile, its start and its 
 // tiles in parts, 24 rows, for which it reads the weights twice, 20.9 and 15.0.  Experts' rows
 // differ in number: 64 experts of 2 x 1280 x 2560 with 8 rows at the mean 157 us, 160 by tiles,
 // with 16 237 and 163; float32 345 and 373, 540 and 382.  The host knows the mean alone: 512 rows of
-// those 64 experts 157 us, 181 with half of them one expert's, 250 with all (float32 356, 421, 509).  SSM_FORCE_PRODUCT_SHAPE and
-// _PARTS override (tests, tuning), for the gradient SSM_FORCE_PRODUCT_PAIR.
+// those 64 experts 157 us, 181 with half of them one expert's, 250 with all (float32 356, 421, 509).
+// SSM_FORCE_PRODUCT_SHAPE and _PARTS override (tests, tuning), for the gradient
+// SSM_FORCE_PRODUCT_PAIR.
 Plan plan_tiles(const ProductArgs& a, int mode) {
   const Sizes z = sizes_of(a, mode);
   Plan q = {kTile64, 1, 0.0};

@@ -46,9 +46,9 @@ def expert_route_fwd(logits, k, score="softmax", renormalize=False, scale=1.0,
     an expert whose logit is -inf is not chosen, and an entry left without one is
     -1 with weight 0), weight [tokens, k] float32 and, with return_score_sum,
     score_sum [experts] float32, every expert's scores summed over the tokens.
-    A NaN counts as the lowest finite logit in the choice; under a softmax it makes
-    its row's weights NaN, chosen or not (so does +inf), under a sigmoid only where
-    it is chosen.  At most 1024 experts and 16 choices.
+    A NaN counts as the lowest finite logit in the choice.  Under a softmax it makes
+    its row's weights NaN, chosen or not (so does +inf); under a sigmoid it does where
+    it is chosen, its own weight or with renormalize the row's.  At most 1024 experts and 16 choices.
     """
     dims = _route_args(logits, k, score, renormalize)
     dev, shape = logits.device, (logits.shape[0], k)
@@ -109,9 +109,9 @@ def expert_sort(index, experts):
     offsets[e + 1] - 1 are expert e's, in the order of (token, choice).
 
     index: [tokens, k] int32; an entry outside 0 .. experts - 1 (a choice that
-    was dropped; expert_route_bwd takes the index with it) has no row.  Returns int32 offsets [experts + 1], token
-    [tokens * k] (every row's token; -1 past offsets[experts]) and slot
-    [tokens, k] (every choice's row; -1 for one without).
+    was dropped; expert_route_bwd takes the index with it) has no row.  Returns
+    int32 offsets [experts + 1], token [tokens * k] (every row's token; -1 past
+    offsets[experts]) and slot [tokens, k] (every choice's row; -1 for one without).
     """
     _gpu(index, "index")
     if index.dim() != 2:
